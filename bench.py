@@ -566,7 +566,8 @@ def rate(shares, kernel, scale):
 # passes per algorithmic product).  The peak is the measured one of the
 # kernel's own arithmetic: bf16 for the bf16 contractions, TF32 (the
 # measured bf16 rate x the nominal dense TF32 / bf16 ratio of B200, 1.1 /
-# 2.25) for the 3 x TF32 GEMM, the fp32 FMA rate of the SMs (148 SMs x 128
+# 2.25) for the 3 x TF32 GEMM, twice the bf16 rate for the int8 product (the
+# nominal dense ratio), the fp32 FMA rate of the SMs (148 SMs x 128
 # lanes x 2 flops x the maximum SM clock) for the SIMT factor kernels, the
 # measured copy bandwidth for the memory-bound ones.  The fraction is
 # algorithmic work / time / that peak; the tensor pipe's own utilisation is
@@ -582,6 +583,8 @@ KERNEL_BOUND = {
     "rtn": ("hbm", "HBM copy", 1),
     "qlinear": ("tensor", "bf16", 2),
     "syrk_bf16": ("tensor", "bf16", 3),
+    "quant_int8": ("hbm", "HBM copy", 1),
+    "w8a8": ("tensor", "int8", 1),
 }
 
 
@@ -596,6 +599,8 @@ def kernel_peak(kernel, peaks, sustained=True):
         return bf16, "TFLOP/s", f"{src} bf16 dense {which}"
     if dtype == "tf32":
         return bf16 * 1.1 / 2.25, "TFLOP/s", f"{src} bf16 dense {which} x 1.1/2.25 (tf32)"
+    if dtype == "int8":
+        return bf16 * 2.0, "TFLOP/s", f"{src} bf16 dense {which} x 4.5/2.25 (int8)"
     if dtype == "fp32 FMA":
         mhz = peaks.get("sm_max_mhz") or 1965.0
         return 148 * 128 * 2 * mhz * 1e6 / 1e12, "TFLOP/s", f"148 SMs x 128 FMA x 2 x {mhz:.0f} MHz"

@@ -364,6 +364,99 @@ gq_status gq_qlinear_bf16(const uint32_t *qpacked, const uint16_t *scales,
                           void *stream);
 
 /* ------------------------------------------------------------------------
+ * Tokens in 8-bit integers: the activations' side of an int8 product.
+ * "Model Quantization Mechanics", section 1: the same symmetric grid as the
+ * weights', with one scale per token, taken from the token itself when the
+ * layer runs.  For a token with the values g_k (fp32)
+ *     s = max_k |g_k| / 127 (IEEE fp32 division; 1 where that is 0),
+ *     c_k = clamp(rint(g_k / s), -127, 127) (IEEE division, half to even),
+ * so codes and scales are bit-exact and deterministic.  A token that holds a
+ * value that is not finite gets codes 0 and scale NaN: its products are NaN,
+ * and no other token is touched.
+ *
+ *   X          [n_tok][ldx] in x_dtype (device, 16-byte aligned; read only),
+ *              of which the first d_in columns are used; ldx >= d_in with
+ *              rows a multiple of 16 bytes long
+ *   d_in       a positive multiple of 16, at most 65536
+ *   codes      [n_tok][d_in] int8 (device, out, 16-byte aligned)
+ *   scales     [n_tok] fp32 (device, out)
+ *   sums       [n_tok] int32 (device, out) or NULL: sum_k c_k, which the
+ *              product with affine weights needs
+ *
+ * gq_quantize_tokens_int8: g = X, or X * col_mul in fp32.
+ *   col_mul    [d_in] fp32 factor per input column (device, 16-byte aligned)
+ *              or NULL; for a layer scaled by gq_awq_rtn_search it is
+ *              1 / col_scale
+ *
+ * gq_rmsnorm_quantize_int8: the residual's addition and the root-mean-square
+ * norm in front of a layer, y = h * weight / sqrt(mean_k h_k^2 + eps) with
+ * h = X + R rounded to x_dtype (h = X without R), written as codes of y.
+ * The row's factor 1 / sqrt(..) divides out of y / s_y, so the codes are
+ * those of g = h * weight (fp32) and only the scale carries the factor:
+ * scale = s / sqrt(mean h^2 + eps), the sum of squares in fp32 (in fp64
+ * where fp32 would overflow or lose it).  Rows are dense (ldx = d_in).
+ *   R          [n_tok][d_in] in x_dtype (device, 16-byte aligned) or NULL
+ *   weight     [d_in] in w_dtype, which is x_dtype or GQ_F32 (device,
+ *              16-byte aligned)
+ *   eps        finite and > 0
+ *   H_out      [n_tok][d_in] in x_dtype (device, out, 16-byte aligned): h;
+ *              given exactly when R is.  It may be X or R itself (in place),
+ *              and must not overlap them otherwise
+ * ---------------------------------------------------------------------- */
+gq_status gq_quantize_tokens_int8(const void *X, gq_dtype x_dtype, int64_t n_tok, int64_t d_in,
+                                  int64_t ldx, const float *col_mul, int8_t *codes,
+                                  float *scales, int32_t *sums, void *stream);
+gq_status gq_rmsnorm_quantize_int8(const void *X, const void *R, gq_dtype x_dtype, int64_t n_tok,
+                                   int64_t d_in, const void *weight, gq_dtype w_dtype, float eps,
+                                   void *H_out, int8_t *codes, float *scales, int32_t *sums,
+                                   void *stream);
+
+/* ------------------------------------------------------------------------
+ * Product of int8 tokens with a layer quantised per output channel:
+ *     acc[t][j] = sum_k x_codes[t][k] w_codes[j][k]       (int32, exact)
+ *     v = x_scale[t] w_scale[j] (acc - w_zpoint[j] x_sum[t]) + bias[j]
+ *     Y[t][j] = act(v) * M[t][j] + R[t][j], in fp32, rounded once to y_dtype.
+ * Every layer that the quantisers above write with group_size -1 or 0 serves
+ * (any `bits`, symmetric or affine, act-order or not); group scales do not,
+ * since a group's scale would have to leave the integer sum.
+ *
+ * gq_unpack_int8 lays such a layer out once: w_codes [d_out][d_in] int8 =
+ * packed code - 2^(bits-1) (a symmetric code is the signed code itself),
+ * w_zpoint [d_out] int32 = zero-point - 2^(bits-1) (affine; NULL when sym).
+ * w_scale is the layer's `scales` array.
+ *   d_in       a positive multiple of 16 (of 32 unless bits is 4), at most
+ *              65536, so that every integer above fits in 32 bits
+ *   w_codes    [d_out][d_in] int8 (device, out, 16-byte aligned); at 8 bits it
+ *              may be qpacked itself (in place), and must not overlap it
+ *              otherwise
+ *
+ * gq_w8a8_matmul:
+ *   w_codes    [d_out][d_in] int8 (device, 16-byte aligned)
+ *   w_scales   [d_out] fp16 bits;  w_zpoint [d_out] int32 or NULL (symmetric)
+ *   x_codes    [n_tok][d_in] int8 (device, 16-byte aligned); x_scales [n_tok]
+ *              fp32; x_sums [n_tok] int32, read only with w_zpoint
+ *   bias       [d_out] fp32 or NULL
+ *   act        GQ_ACT_NONE, GQ_ACT_RELU, GQ_ACT_GELU or GQ_ACT_SILU
+ *              (v / (1 + e^-v)); NaN stays NaN
+ *   M, R       [n_tok][d_out] in y_dtype (device, 16-byte aligned) or NULL: a
+ *              factor (the other branch of a gated MLP) and a residual; either
+ *              may be Y itself
+ *   Y          [n_tok][d_out] in y_dtype (device, out, 16-byte aligned)
+ *   ws         >= gq_w8a8_workspace_size(d_out, d_in, n_tok) bytes (the
+ *              device status word only)
+ * ---------------------------------------------------------------------- */
+enum { GQ_ACT_SILU = 3 };  /* gq_w8a8_matmul only */
+gq_status gq_unpack_int8(const uint32_t *qpacked, const uint16_t *zeros, int64_t d_out,
+                         int64_t d_in, int bits, int sym, int8_t *w_codes, int32_t *w_zpoint,
+                         void *stream);
+size_t gq_w8a8_workspace_size(int64_t d_out, int64_t d_in, int64_t n_tok);
+gq_status gq_w8a8_matmul(const int8_t *w_codes, const uint16_t *w_scales, const int32_t *w_zpoint,
+                         int64_t d_out, int64_t d_in, const int8_t *x_codes,
+                         const float *x_scales, const int32_t *x_sums, int64_t n_tok,
+                         const float *bias, int act, const void *M, const void *R, void *Y,
+                         gq_dtype y_dtype, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
  * Sequential quantisation of a chain of layers, each calibrated on the input
  * it actually receives: the output of the already quantised layers before
  * it ("GPT-2 Quantization Reconstruction Error", "Key findings": the
@@ -504,10 +597,12 @@ gq_status gq_selftest_bounded_wait(int arrive, uint64_t limit_ns, void *ws, size
  * GEMM_TF32X3 (the fp32 product; lower-triangle calls count the triangle),
  * RECON_MMA (one product (W - W^) X^T), QLINEAR (one product W^ X^T:
  * 2 n_tok d_out d_in) and SYRK_BF16 (the lower triangle of dW^T dW in the
- * error from the Hessian, three bf16 products: d_in (d_in + 1) d_out),
+ * error from the Hessian, three bf16 products: d_in (d_in + 1) d_out) and
+ * W8A8 (integer operations, 2 n_tok d_out d_in),
  * and in bytes that must cross
  * HBM for GPTQ_BLOCK (the block's working weights read, Err written, the U
- * block, codes and scales) and RTN (W read, codes, scales and zeros
+ * block, codes and scales), RTN (W read, codes, scales and zeros
+ * written) and QUANT_INT8 (X, R and factors read, H, codes, scales and sums
  * written).  One session at a time per process; the calls are thread safe.
  * ---------------------------------------------------------------------- */
 typedef enum {
@@ -520,7 +615,9 @@ typedef enum {
   GQ_KERNEL_RECON_MMA = 6,
   GQ_KERNEL_QLINEAR = 7,
   GQ_KERNEL_SYRK_BF16 = 8,
-  GQ_KERNEL_COUNT = 9
+  GQ_KERNEL_QUANT_INT8 = 9,
+  GQ_KERNEL_W8A8 = 10,
+  GQ_KERNEL_COUNT = 11
 } gq_kernel;
 
 gq_status gq_kernel_timer_start(uint32_t mask, int32_t capacity);

@@ -81,7 +81,7 @@ __all__ = [
     "round_to_grid", "round_error_carried_forward", "gptq_fixed_grid",
     "gptq_layer", "awq_channel_scales", "awq_apply", "awq_rtn_search", "w4a16_matmul",
     "round_to_bf16", "gelu_tanh", "apply_layer", "gptq_sequential", "TIE_TOL", "TIE_REL",
-    "QUOT_REL",
+    "QUOT_REL", "quantize_rows_int8", "rmsnorm_int8", "w8a8_matmul",
 ]
 
 
@@ -828,3 +828,62 @@ def gptq_fixed_grid(w_row, X, step, damp_percent=0.01, block_size=128):
         w[:, b0:b1] = Wb
         w[:, b1:] -= Err @ U[b0:b1, b1:]
     return Q[0]
+
+
+# --------------------------------------------------------------------------
+# 8-bit tokens and their product with a layer
+# --------------------------------------------------------------------------
+
+def quantize_rows_int8(G):
+    """Codes, steps and code sums of the rows of G (fp32 values): s = max |g| / 127 (1 where that is
+    0), c = clamp(rint(g / s), -127, 127), both quotients in IEEE float32 (the symmetric grid of
+    "Model Quantization Mechanics", section 1, with one scale per row).  A row with a value that is
+    not finite: codes 0, step NaN."""
+    G = np.asarray(G, dtype=F32)
+    bad = ~np.all(np.isfinite(G), axis=1)
+    G = np.where(bad[:, None], F32(0), G)
+    with np.errstate(under="ignore"):
+        s = np.max(np.abs(G), axis=1) / F32(127)
+        s = np.where(s == 0, F32(1), s).astype(F32)
+        c = np.clip(np.rint(G / s[:, None]), -127, 127).astype(np.int64)
+    return c.astype(np.int8), np.where(bad, F32(np.nan), s), c.sum(axis=1)
+
+
+def rmsnorm_int8(X, weight, eps, R=None, round_to=None):
+    """(h, codes, scales in fp64, sums) of y = h * weight / sqrt(mean h^2 + eps), h = X + R rounded
+    by ``round_to``.  The row's factor divides out of y / s_y, so the codes are those of the fp32
+    products h * weight and the scale is their step times the factor."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        h = np.asarray(X, dtype=F32)
+        if R is not None:
+            h = round_to(h + np.asarray(R, dtype=F32))
+        g = h * np.asarray(weight, dtype=F32)
+        codes, s, sums = quantize_rows_int8(g)
+        h64 = h.astype(np.float64)
+        f = 1.0 / np.sqrt(np.mean(h64 * h64, axis=1) + np.float64(F32(eps)))
+    return h, codes, s.astype(np.float64) * f, sums
+
+
+def w8a8_matmul(w_codes, w_scales, w_zpoint, x_codes, x_scales, bias=None, act="none", M=None,
+                R=None) -> np.ndarray:
+    """act(x W^T + bias) * M + R in fp64 from integer codes: the integer sums in int64."""
+    c = np.asarray(w_codes, dtype=np.int64)
+    if w_zpoint is not None:
+        c = c - np.asarray(w_zpoint, dtype=np.int64)[:, None]
+    acc = np.asarray(x_codes, dtype=np.int64).astype(np.float64) @ c.T.astype(np.float64)
+    v = acc * np.asarray(w_scales, dtype=np.float64).reshape(1, -1)
+    v = v * np.asarray(x_scales, dtype=np.float64).reshape(-1, 1)
+    if bias is not None:
+        v = v + np.asarray(bias, dtype=np.float64)
+    if act == "relu":
+        v = np.where(v < 0, 0.0, v)
+    elif act == "gelu":
+        v = gelu_tanh(v)
+    elif act == "silu":
+        with np.errstate(over="ignore"):
+            v = v / (1.0 + np.exp(-v))
+    if M is not None:
+        v = v * np.asarray(M, dtype=np.float64)
+    if R is not None:
+        v = v + np.asarray(R, dtype=np.float64)
+    return v

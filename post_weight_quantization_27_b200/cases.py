@@ -4,7 +4,7 @@ stage by hand.
 
     python -m post_weight_quantization_27_b200.cases --workload 2 --layer 3
            [--tokens N] [--repeat R]
-           [--stages hessian,solve,gptq,rtn,recon,trace,awq,w4a16,qlinear]
+           [--stages hessian,solve,gptq,rtn,recon,trace,awq,w4a16,qlinear,int8,w8a8]
 
 The stages always run in path order (H -> damp/U -> GPTQ -> RTN -> recon),
 each as many times as --repeat says; a stage that is not listed still runs
@@ -14,7 +14,9 @@ and RTN layers; "trace" is the error from the Hessian (tr(dW H dW^T) / 2) of
 the GPTQ layer (of the RTN layer when GPTQ is not listed); "awq" is the
 activation-aware scaling search before RTN (20 values of alpha), which needs
 only H; "w4a16" multiplies the RTN layer with the first (at most 8192)
-tokens; "qlinear" applies it to them (token-major bf16 output, GELU).
+tokens; "qlinear" applies it to them (token-major bf16 output, GELU); "int8"
+quantises these tokens to int8 and "w8a8" multiplies them with the layer in
+8-bit RTN codes, one scale per output channel.
 """
 from __future__ import annotations
 
@@ -25,7 +27,8 @@ import torch
 from . import gq
 from . import inputs as I
 
-ORDER = ("hessian", "solve", "gptq", "rtn", "recon", "trace", "awq", "w4a16", "qlinear")
+ORDER = ("hessian", "solve", "gptq", "rtn", "recon", "trace", "awq", "w4a16", "qlinear",
+         "int8", "w8a8")
 
 
 def run(workload: int, layer: int, tokens: int | None, stages, repeat: int = 1) -> dict:
@@ -38,7 +41,7 @@ def run(workload: int, layer: int, tokens: int | None, stages, repeat: int = 1) 
     deps = {"hessian": set(), "solve": {"hessian"}, "gptq": {"hessian", "solve"}, "rtn": set(),
             "recon": {"hessian", "solve", "gptq", "rtn"}, "awq": {"hessian"},
             "trace": {"hessian"} | ({"solve", "gptq"} if "gptq" in stages else {"rtn"}),
-            "w4a16": {"rtn"}, "qlinear": {"rtn"}}
+            "w4a16": {"rtn"}, "qlinear": {"rtn"}, "int8": set(), "w8a8": {"int8"}}
     need = set(stages)
     for st in stages:
         need |= deps[st]
@@ -83,6 +86,12 @@ def run(workload: int, layer: int, tokens: int | None, stages, repeat: int = 1) 
         Xs = X[:min(X.shape[0], 8192)]
         timed("qlinear", lambda: gq.qlinear_bf16(Xs, spec.d_out, q=r, group_size=spec.group_size,
                                                  sym=spec.sym, act="gelu"))
+    if "int8" in need:
+        Xs = X[:min(X.shape[0], 8192)]
+        x8 = timed("int8", lambda: gq.quantize_tokens_int8(Xs))
+    if "w8a8" in need:
+        w8 = gq.unpack_int8(gq.rtn_quantize_pack(W, 8, -1, spec.sym), spec.d_in, -1, spec.sym)
+        timed("w8a8", lambda: gq.w8a8_matmul(w8, x8, act="gelu"))
     return {"spec": spec, "ms": times}
 
 

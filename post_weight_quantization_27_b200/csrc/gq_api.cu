@@ -433,6 +433,111 @@ gq_status gq_qlinear_bf16(const uint32_t *qpacked, const uint16_t *scales,
                         static_cast<int *>(ws), static_cast<cudaStream_t>(stream));
 }
 
+namespace {
+gq_status check_tokens8(int64_t n_tok, int64_t d_in) {
+  if (n_tok < 0 || n_tok > (int64_t(1) << 31) - 256) return fail(GQ_ERR_SHAPE, "bad n_tok");
+  if (d_in < 16 || d_in % 16 != 0 || d_in > 65536)
+    return fail(GQ_ERR_SHAPE, "int8 tokens need d_in a positive multiple of 16, at most 65536");
+  return GQ_OK;
+}
+size_t dtype_size(gq_dtype dt) { return dt == GQ_F32 ? 4 : 2; }
+// Whether [a, a + bytes) and [b, b + bytes) share a byte without being one range.
+bool partly_overlap(const void *a, const void *b, uint64_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x != y && (x < y ? y - x : x - y) < bytes;
+}
+}  // namespace
+
+gq_status gq_quantize_tokens_int8(const void *X, gq_dtype x_dtype, int64_t n_tok, int64_t d_in,
+                                  int64_t ldx, const float *col_mul, int8_t *codes,
+                                  float *scales, int32_t *sums, void *stream) {
+  t_last_error.clear();
+  GQ_TRY(check_dtype(x_dtype));
+  GQ_TRY(check_tokens8(n_tok, d_in));
+  if (n_tok > 0 && (!X || !codes || !scales)) return fail(GQ_ERR_ARG, "null pointer");
+  if (ldx < d_in || ldx > (int64_t(1) << 40) || ldx * dtype_size(x_dtype) % 16 != 0)
+    return fail(GQ_ERR_SHAPE, "ldx must be at least d_in, with rows a multiple of 16 bytes long");
+  if (!aligned(X, 16) || !aligned(col_mul, 16) || !aligned(codes, 16))
+    return fail(GQ_ERR_ARG, "X, col_mul and codes must be 16-byte aligned");
+  return launch_quant_int8(X, nullptr, x_dtype, n_tok, d_in, ldx, col_mul, GQ_F32, 0, 0.0f,
+                           nullptr, codes, scales, sums, static_cast<cudaStream_t>(stream));
+}
+
+gq_status gq_rmsnorm_quantize_int8(const void *X, const void *R, gq_dtype x_dtype, int64_t n_tok,
+                                   int64_t d_in, const void *weight, gq_dtype w_dtype, float eps,
+                                   void *H_out, int8_t *codes, float *scales, int32_t *sums,
+                                   void *stream) {
+  t_last_error.clear();
+  GQ_TRY(check_dtype(x_dtype));
+  if (w_dtype != GQ_F32 && w_dtype != x_dtype)
+    return fail(GQ_ERR_DTYPE, "the weight's dtype must be X's or GQ_F32");
+  GQ_TRY(check_tokens8(n_tok, d_in));
+  if (!weight || (n_tok > 0 && (!X || !codes || !scales))) return fail(GQ_ERR_ARG, "null pointer");
+  if (!(eps > 0.0f) || !(eps < 1e30f)) return fail(GQ_ERR_ARG, "eps must be finite and > 0");
+  if (n_tok > 0 && (R == nullptr) != (H_out == nullptr))
+    return fail(GQ_ERR_ARG, "H_out goes with R: both or neither");
+  if (!aligned(X, 16) || !aligned(R, 16) || !aligned(weight, 16) || !aligned(H_out, 16) ||
+      !aligned(codes, 16))
+    return fail(GQ_ERR_ARG, "X, R, weight, H_out and codes must be 16-byte aligned");
+  const uint64_t bytes = static_cast<uint64_t>(n_tok) * d_in * dtype_size(x_dtype);
+  if (partly_overlap(H_out, X, bytes) || partly_overlap(H_out, R, bytes))
+    return fail(GQ_ERR_ARG, "H_out must be X, R or a range of its own");
+  return launch_quant_int8(X, R, x_dtype, n_tok, d_in, d_in, weight, w_dtype, 1, eps, H_out, codes,
+                           scales, sums, static_cast<cudaStream_t>(stream));
+}
+
+gq_status gq_unpack_int8(const uint32_t *qpacked, const uint16_t *zeros, int64_t d_out,
+                         int64_t d_in, int bits, int sym, int8_t *w_codes, int32_t *w_zpoint,
+                         void *stream) {
+  t_last_error.clear();
+  if (!qpacked || !w_codes) return fail(GQ_ERR_ARG, "null pointer");
+  if (sym != 0 && sym != 1) return fail(GQ_ERR_ARG, "sym must be 0 or 1");
+  if (sym == 0 && (!zeros || !w_zpoint))
+    return fail(GQ_ERR_ARG, "an affine layer needs zeros and w_zpoint");
+  GQ_TRY(check_layer(d_out, d_in));
+  GQ_TRY(check_bits(bits, d_in, -1));
+  GQ_TRY(check_tokens8(0, d_in));
+  if (!aligned(w_codes, 16)) return fail(GQ_ERR_ARG, "w_codes must be 16-byte aligned");
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(qpacked), c0 = reinterpret_cast<uintptr_t>(w_codes);
+  const uint64_t qn = static_cast<uint64_t>(d_out) * d_in * bits / 8, cn = static_cast<uint64_t>(d_out) * d_in;
+  if (q0 < c0 + cn && c0 < q0 + qn && !(bits == 8 && q0 == c0))
+    return fail(GQ_ERR_ARG, "w_codes must not overlap qpacked (at 8 bits it may be qpacked itself)");
+  return launch_unpack_int8(qpacked, zeros, d_out, d_in, bits, w_codes, sym ? nullptr : w_zpoint,
+                            static_cast<cudaStream_t>(stream));
+}
+
+size_t gq_w8a8_workspace_size(int64_t d_out, int64_t d_in, int64_t n_tok) {
+  if (d_out < 1 || d_in < 16 || d_in % 16 != 0 || d_in > 65536 || n_tok < 0) return 0;
+  return kWsHeader;
+}
+
+gq_status gq_w8a8_matmul(const int8_t *w_codes, const uint16_t *w_scales, const int32_t *w_zpoint,
+                         int64_t d_out, int64_t d_in, const int8_t *x_codes,
+                         const float *x_scales, const int32_t *x_sums, int64_t n_tok,
+                         const float *bias, int act, const void *M, const void *R, void *Y,
+                         gq_dtype y_dtype, void *ws, size_t ws_bytes, void *stream) {
+  t_last_error.clear();
+  GQ_TRY(check_dtype(y_dtype));
+  GQ_TRY(check_layer(d_out, d_in));
+  GQ_TRY(check_tokens8(n_tok, d_in));
+  if (d_out > (int64_t(1) << 31) - 256) return fail(GQ_ERR_SHAPE, "bad d_out");
+  if (!w_codes || !w_scales || (n_tok > 0 && (!x_codes || !x_scales || !Y)))
+    return fail(GQ_ERR_ARG, "null pointer");
+  if (w_zpoint && n_tok > 0 && !x_sums) return fail(GQ_ERR_ARG, "an affine layer needs x_sums");
+  if (act < GQ_ACT_NONE || act > GQ_ACT_SILU)
+    return fail(GQ_ERR_ARG, "act must be GQ_ACT_NONE, GQ_ACT_RELU, GQ_ACT_GELU or GQ_ACT_SILU");
+  if (!aligned(w_codes, 16) || !aligned(x_codes, 16) || !aligned(M, 16) || !aligned(R, 16) ||
+      !aligned(Y, 16))
+    return fail(GQ_ERR_ARG, "w_codes, x_codes, M, R and Y must be 16-byte aligned");
+  const uint64_t bytes = static_cast<uint64_t>(n_tok) * d_out * dtype_size(y_dtype);
+  if (partly_overlap(Y, M, bytes) || partly_overlap(Y, R, bytes))
+    return fail(GQ_ERR_ARG, "Y must be M, R or a range of its own");
+  GQ_TRY(check_ws(ws, ws_bytes, kWsHeader));
+  return launch_w8a8(w_codes, w_scales, w_zpoint, d_out, d_in, x_codes, x_scales, x_sums, n_tok,
+                     bias, act, M, R, Y, y_dtype, static_cast<int *>(ws),
+                     static_cast<cudaStream_t>(stream));
+}
+
 size_t gq_gptq_sequential_workspace_size(const gq_seq_layer *layers, int n_layers,
                                          int64_t n_tok, int block_size) {
   if (!layers || n_layers < 1 || n_tok < 0) return 0;

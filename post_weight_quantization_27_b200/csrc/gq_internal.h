@@ -124,6 +124,21 @@ gq_status launch_qlinear(const uint32_t *qpacked, const uint16_t *scales, const 
                          const void *X, int64_t n_tok, float *Y, void *Z, const void *R,
                          int act, int *status, cudaStream_t st);
 
+// Tokens as int8 codes with a scale each (quant8.cu); norm: behind the
+// residual's addition and the root-mean-square norm.
+gq_status launch_quant_int8(const void *X, const void *R, gq_dtype dt, int64_t n_tok, int64_t d_in,
+                            int64_t ldx, const void *w, gq_dtype w_dtype, int norm, float eps,
+                            void *H, int8_t *codes, float *scales, int32_t *sums, cudaStream_t st);
+gq_status launch_unpack_int8(const uint32_t *qpacked, const uint16_t *zeros, int64_t d_out,
+                             int64_t d_in, int bits, int8_t *codes, int32_t *zpoint,
+                             cudaStream_t st);
+// The int8 product (w8a8.cu).
+gq_status launch_w8a8(const int8_t *w_codes, const uint16_t *w_scales, const int32_t *w_zpoint,
+                      int64_t d_out, int64_t d_in, const int8_t *x_codes, const float *x_scales,
+                      const int32_t *x_sums, int64_t n_tok, const float *bias, int act,
+                      const void *M, const void *R, void *Y, gq_dtype y_dtype, int *status,
+                      cudaStream_t st);
+
 // Sequential quantisation of a chain of layers (pipeline.cu).
 size_t seq_ws_bytes(const gq_seq_layer *layers, int n_layers, int64_t n_tok, int block_size);
 gq_status launch_sequential(const void *X0, int64_t n_tok, const gq_seq_layer *layers, int n,

@@ -97,6 +97,19 @@ def lib() -> ctypes.CDLL:
     L.gq_qlinear_bf16.argtypes = [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_i64, _c_i64,
                                   _c_int, _c_int, _c_int, _c_vp, _c_i64, _c_int, _c_vp, _c_vp,
                                   _c_vp, _c_sz, _c_vp]
+    L.gq_quantize_tokens_int8.restype = _c_int
+    L.gq_quantize_tokens_int8.argtypes = [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp,
+                                          _c_vp, _c_vp, _c_vp]
+    L.gq_rmsnorm_quantize_int8.restype = _c_int
+    L.gq_rmsnorm_quantize_int8.argtypes = [_c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_int,
+                                           _c_f32, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]
+    L.gq_unpack_int8.restype = _c_int
+    L.gq_unpack_int8.argtypes = [_c_vp, _c_vp, _c_i64, _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_vp]
+    L.gq_w8a8_workspace_size.restype = _c_sz
+    L.gq_w8a8_workspace_size.argtypes = [_c_i64, _c_i64, _c_i64]
+    L.gq_w8a8_matmul.restype = _c_int
+    L.gq_w8a8_matmul.argtypes = [_c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_i64,
+                                 _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_sz, _c_vp]
     L.gq_gptq_sequential_workspace_size.restype = _c_sz
     L.gq_gptq_sequential_workspace_size.argtypes = [_c_vp, _c_int, _c_i64, _c_int]
     L.gq_gptq_sequential.restype = _c_int
@@ -130,7 +143,9 @@ EXPORTS = ("gq_status_string", "gq_last_error", "gq_launch_count", "gq_hessian_w
            "gq_gptq_workspace_size", "gq_gptq_quantize_layer", "gq_rtn_quantize_pack",
            "gq_recon_workspace_size", "gq_recon_error", "gq_recon_error_hessian_workspace_size",
            "gq_recon_error_hessian", "gq_w4a16_workspace_size",
-           "gq_w4a16_matmul", "gq_qlinear_bf16", "gq_gptq_sequential_workspace_size",
+           "gq_w4a16_matmul", "gq_qlinear_bf16", "gq_quantize_tokens_int8",
+           "gq_rmsnorm_quantize_int8", "gq_unpack_int8", "gq_w8a8_workspace_size",
+           "gq_w8a8_matmul", "gq_gptq_sequential_workspace_size",
            "gq_gptq_sequential", "gq_awq_workspace_size",
            "gq_awq_rtn_search", "gq_workspace_status", "gq_selftest_bounded_wait",
            "gq_kernel_timer_start",
@@ -450,6 +465,177 @@ def qlinear_bf16(X: torch.Tensor, d_out: int, q: dict | None = None, W: torch.Te
     return Z
 
 
+# ------------------------------------------------------------------ int8 tokens and their products
+
+ACT8 = dict(ACT, silu=3)
+
+
+def _on_current(t: torch.Tensor, name: str) -> torch.Tensor:
+    """Refuses a tensor of another device than the current one: the launch would go to the current
+    device's stream."""
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return t
+
+
+def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """A tensor that a call on ``stream`` writes: where that is not the current stream, the allocator
+    is told, so that the memory is not handed out again before that stream's work is done."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _tokens8(X: torch.Tensor, n_tok: int, d_in: int, with_sums: bool, out, stream):
+    """(codes, scales, sums or None) for n_tok tokens: those of ``out``, checked, or new ones."""
+    if out is None:
+        return (_new((n_tok, d_in), torch.int8, X, stream), _new((n_tok,), torch.float32, X, stream),
+                _new((n_tok,), torch.int32, X, stream) if with_sums else None)
+    sums = out.get("sums")
+    return (_on_current(_dev(out["codes"], "codes", torch.int8, (n_tok, d_in)), "codes"),
+            _on_current(_dev(out["scales"], "scales", torch.float32, (n_tok,)), "scales"),
+            None if sums is None else _on_current(_dev(sums, "sums", torch.int32, (n_tok,)), "sums"))
+
+
+def quantize_tokens_int8(X: torch.Tensor, col_mul: torch.Tensor | None = None,
+                         with_sums: bool = True, out: dict | None = None, stream=None) -> dict:
+    """Tokens X [n_tok][d_in] (fp32, fp16 or bf16; rows may be a slice of wider ones) as int8 codes
+    with one scale each.  ``col_mul`` (fp32 [d_in]) multiplies the columns first: 1 / col_scale of
+    awq_rtn_search's layers.  Returns dict(codes, scales, sums): sums (the codes' sums, which affine
+    weights need) is None without ``with_sums``.  With ``out`` those tensors are written (sums where
+    it has them)."""
+    if not isinstance(X, torch.Tensor) or not X.is_cuda or X.dim() != 2:
+        raise ValueError("X must be a CUDA tensor [n_tok][d_in]")
+    dt = _DTYPES.get(X.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported X dtype {X.dtype}")
+    _on_current(X, "X")
+    n_tok, d_in = X.shape
+    ldx, one = X.stride()
+    if n_tok <= 1:
+        ldx = d_in
+    if one != 1 and d_in > 1:
+        raise ValueError("X's columns must be adjacent")
+    if col_mul is not None:
+        _on_current(_dev(col_mul, "col_mul", torch.float32, (d_in,)), "col_mul")
+    codes, scales, sums = _tokens8(X, n_tok, d_in, with_sums, out, stream)
+    st = lib().gq_quantize_tokens_int8(_p(X), dt, n_tok, d_in, ldx, _p(col_mul), _p(codes),
+                                       _p(scales), _p(sums), _stream(stream))
+    if st:
+        _check(st, "gq_quantize_tokens_int8")
+    return dict(codes=codes, scales=scales, sums=sums)
+
+
+def rmsnorm_quantize_int8(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
+                          R: torch.Tensor | None = None, H: torch.Tensor | None = None,
+                          with_sums: bool = True, out: dict | None = None, stream=None) -> dict:
+    """y = h * weight / sqrt(mean h^2 + eps) with h = X + R (rounded to X's dtype; h = X without R)
+    as int8 codes with one scale per token.  Returns dict(codes, scales, sums, h): h is the sum,
+    written to ``H`` (which may be X or R) or to a new tensor; X itself without R.  ``out`` as for
+    quantize_tokens_int8."""
+    _on_current(_dev(X, "X"), "X")
+    dt = _DTYPES.get(X.dtype)
+    if dt is None or X.dim() != 2:
+        raise ValueError(f"X must be [n_tok][d_in] in fp32, fp16 or bf16, got {X.dtype}")
+    n_tok, d_in = X.shape
+    _on_current(_dev(weight, "weight", None, (d_in,)), "weight")
+    if weight.dtype not in _DTYPES:
+        raise ValueError(f"unsupported weight dtype {weight.dtype}")
+    if R is not None:
+        _on_current(_dev(R, "R", X.dtype, (n_tok, d_in)), "R")
+        H = _new((n_tok, d_in), X.dtype, X, stream) if H is None else \
+            _on_current(_dev(H, "H", X.dtype, (n_tok, d_in)), "H")
+    elif H is not None:
+        raise ValueError("H is written only with a residual R")
+    codes, scales, sums = _tokens8(X, n_tok, d_in, with_sums, out, stream)
+    st = lib().gq_rmsnorm_quantize_int8(_p(X), _p(R), dt, n_tok, d_in, _p(weight),
+                                        _DTYPES[weight.dtype], eps, _p(H), _p(codes), _p(scales),
+                                        _p(sums), _stream(stream))
+    if st:
+        _check(st, "gq_rmsnorm_quantize_int8")
+    return dict(codes=codes, scales=scales, sums=sums, h=X if H is None else H)
+
+
+def unpack_int8(q: dict, d_in: int, group_size: int = -1, sym: bool = True, stream=None) -> dict:
+    """A quantised layer ``q`` (dict as returned by the quantisers, one scale per output channel:
+    group_size -1 or 0) laid out for w8a8_matmul: dict(codes int8 [d_out][d_in], scales fp16,
+    zpoint int32 [d_out] or None).  Done once per layer; the scales are q's own tensor."""
+    if group_size not in (-1, 0):
+        raise ValueError("an int8 product needs one scale per output channel: group_size -1 or 0")
+    bits = int(q.get("bits", 4))
+    qp = _on_current(_dev(q["qpacked"], "qpacked", torch.int32), "qpacked")
+    d_out = qp.shape[0]
+    if tuple(qp.shape) != (d_out, bits * d_in // 32):
+        raise ValueError(f"qpacked must have shape {(d_out, bits * d_in // 32)}, got {tuple(qp.shape)}")
+    _dev(q["scales"], "scales", torch.float16, (d_out, 1))
+    if not sym:
+        _dev(q["zeros"], "zeros", torch.float16, (d_out, 1))
+    codes = _new((d_out, d_in), torch.int8, qp, stream)
+    zp = None if sym else _new((d_out,), torch.int32, qp, stream)
+    st = lib().gq_unpack_int8(_p(qp), None if sym else _p(q["zeros"]), d_out, d_in, bits,
+                              int(bool(sym)), _p(codes), _p(zp), _stream(stream))
+    _check(st, "gq_unpack_int8")
+    return dict(codes=codes, scales=q["scales"], zpoint=zp)
+
+
+def w8a8_workspace_size(d_out: int, d_in: int, n_tok: int) -> int:
+    return int(lib().gq_w8a8_workspace_size(d_out, d_in, n_tok))
+
+
+def w8a8_matmul(w: dict, x: dict, bias: torch.Tensor | None = None, act: str = "none",
+                mul: torch.Tensor | None = None, R: torch.Tensor | None = None,
+                Y: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16,
+                ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y [n_tok][d_out] = act(x W^T + bias) * mul + R from int8 tokens ``x`` (dict of
+    quantize_tokens_int8 or rmsnorm_quantize_int8) and an int8 layer ``w`` (dict of unpack_int8).
+    bias is fp32 [d_out]; mul and R have Y's shape and dtype (``dtype`` when Y is not given) and may
+    be Y itself; act is "none", "relu", "gelu" or "silu"."""
+    wc, xc = w["codes"], x["codes"]
+    _on_current(_dev(xc, "x codes", torch.int8), "x codes")
+    _on_current(_dev(wc, "w codes", torch.int8), "w codes")
+    n_tok, d_in = xc.shape
+    d_out = wc.shape[0]
+    if wc.shape[1] != d_in:
+        raise ValueError(f"the layer has {wc.shape[1]} inputs, the tokens {d_in}")
+    wsc, xsc, zp, sums = w["scales"], x["scales"], w.get("zpoint"), None
+    _dev(wsc, "w scales", torch.float16)
+    _dev(xsc, "x scales", torch.float32)
+    if wsc.numel() != d_out or xsc.numel() != n_tok:
+        raise ValueError("one scale per output channel and one per token are needed")
+    if zp is not None:
+        _dev(zp, "zpoint", torch.int32, (d_out,))
+        sums = x.get("sums")
+        if sums is None:
+            raise ValueError("an affine layer needs the tokens' sums (with_sums=True)")
+        _dev(sums, "sums", torch.int32, (n_tok,))
+    if act not in ACT8:
+        raise ValueError(f"act must be one of {', '.join(ACT8)}")
+    shape = (n_tok, d_out)
+    if Y is None:
+        Y = _new(shape, dtype, xc, stream)
+    else:
+        _on_current(_dev(Y, "Y", None, shape), "Y")
+    dt = _DTYPES.get(Y.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported Y dtype {Y.dtype}")
+    if bias is not None:
+        _dev(bias, "bias", torch.float32, (d_out,))
+    if mul is not None:
+        _dev(mul, "mul", Y.dtype, shape)
+    if R is not None:
+        _dev(R, "R", Y.dtype, shape)
+    if ws is None:
+        ws = _new((256,), torch.uint8, xc, stream)
+    st = lib().gq_w8a8_matmul(_p(wc), _p(wsc), _p(zp), d_out, d_in, _p(xc), _p(xsc), _p(sums), n_tok,
+                              _p(bias), ACT8[act], _p(mul), _p(R), _p(Y), dt, _p(ws), ws.numel(),
+                              _stream(stream))
+    if st:
+        _check(st, "gq_w8a8_matmul")
+    return Y
+
+
 # ------------------------------------------------------------------ sequential quantisation
 
 def gptq_sequential(X0: torch.Tensor, layers: list, bits: int = 4, group_size: int = -1,
@@ -534,10 +720,10 @@ def awq_rtn_search(W: torch.Tensor, H: torch.Tensor, X: torch.Tensor, bits: int 
 
 # gq_kernel values (include/gq.h) and the unit of each kernel's work figure
 KERNELS = ("hessian_mma", "potrf_trsm", "block_inverse", "gemm_tf32x3", "gptq_block", "rtn",
-           "recon_mma", "qlinear", "syrk_bf16")
+           "recon_mma", "qlinear", "syrk_bf16", "quant_int8", "w8a8")
 KERNEL_UNITS = {"hessian_mma": "flop", "potrf_trsm": "flop", "block_inverse": "flop",
                 "gemm_tf32x3": "flop", "gptq_block": "byte", "rtn": "byte", "recon_mma": "flop",
-                "qlinear": "flop", "syrk_bf16": "flop"}
+                "qlinear": "flop", "syrk_bf16": "flop", "quant_int8": "byte", "w8a8": "flop"}
 
 
 def kernel_timer_start(kernels, capacity: int) -> None:
