@@ -521,6 +521,7 @@ gq_status gq_w8a8_matmul(const int8_t *w_codes, const uint16_t *w_scales, const 
   GQ_TRY(check_layer(d_out, d_in));
   GQ_TRY(check_tokens8(n_tok, d_in));
   if (d_out > (int64_t(1) << 31) - 256) return fail(GQ_ERR_SHAPE, "bad d_out");
+  if (n_tok > (int64_t(1) << 40) / d_out) return fail(GQ_ERR_SHAPE, "n_tok * d_out above 2^40");
   if (!w_codes || !w_scales || (n_tok > 0 && (!x_codes || !x_scales || !Y)))
     return fail(GQ_ERR_ARG, "null pointer");
   if (w_zpoint && n_tok > 0 && !x_sums) return fail(GQ_ERR_ARG, "an affine layer needs x_sums");
