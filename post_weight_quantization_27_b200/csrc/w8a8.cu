@@ -56,13 +56,19 @@ __device__ __forceinline__ void from_f(float v, float &o) { o = v; }
 __device__ __forceinline__ void from_f(float v, __half &o) { o = __float2half_rn(v); }
 __device__ __forceinline__ void from_f(float v, __nv_bfloat16 &o) { o = __float2bfloat16_rn(v); }
 
-// One output element.  The product is taken as (v w_scale) x_scale: |v| <
+// The device status word, cleared by the launch's first block as it starts:
+// a wait gives up 2 s after that at the earliest.
+__device__ __forceinline__ void reset_status(int *status) { *reinterpret_cast<volatile int *>(status) = 0; }
+
+// Output j of token t from its integer sum and the output's own scale,
+// zero-point and bias.  The product is taken as (v w_scale) x_scale: |v| <
 // 2^31 times an fp16 scale neither overflows nor loses a normal result.
 template <typename T>
-__device__ __forceinline__ void finish(const W8Args &a, int64_t t, int64_t j, int acc) {
-  if (a.wz) acc = sub_wrap(acc, a.wz[j], a.xsum[t]);
-  float v = static_cast<float>(acc) * __half2float(__ushort_as_half(a.ws[j])) * a.xs[t];
-  if (a.bias) v += a.bias[j];
+__device__ __forceinline__ void finish(const W8Args &a, int64_t t, int64_t j, int acc, float ws,
+                                       int wz, float bias) {
+  if (a.wz) acc = sub_wrap(acc, wz, a.xsum[t]);
+  float v = static_cast<float>(acc) * ws * a.xs[t];
+  if (a.bias) v += bias;
   v = act8(v, a.act);
   const int64_t i = t * a.d_out + j;
   if (a.m) v *= to_f(static_cast<const T *>(a.m)[i]);
@@ -241,6 +247,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
   const int pair = static_cast<int>(blockIdx.x >> 1), n_pairs = static_cast<int>(gridDim.x >> 1);
   const int n_tiles = a.n_tt * a.n_jt;
   if (threadIdx.x == 0) {
+    if (blockIdx.x == 0) reset_status(a.status);
     for (int s = 0; s < P_STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -401,51 +408,150 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
   }
 }
 
-// 64 x 64 outputs per block of 256 threads, 4 x 4 per thread, K in steps of
-// 64 bytes through shared memory.
+// ---------------------------------------------------------------- few tiles
+// 128 outputs x up to 128 tokens per cluster of `split` CTAs, each summing
+// its own range of K on the tensor cores (M = the outputs, N = the tokens
+// rounded up to 16, so a short batch wastes no operand rows); two or more
+// CTAs fit an SM, so one's epilogue runs beside another's loads.  With
+// split > 1 every CTA lays its integer sums out in its (then idle) ring,
+// and CTA r of the cluster adds the token columns r, r + split, .. of all
+// of them over distributed shared memory: integers, so the order of the
+// additions does not matter, no workspace and no second launch.
+// A lane owns an output, so a warp's accesses to Y, M and R are contiguous
+// whatever d_out is.
+constexpr int F_J = 128, F_T = 128, F_MAX_STAGES = 8, F_THREADS = 128;
+
+struct FewPlan {
+  int bn;            // tokens per tile, a multiple of 16
+  int stages, split;
+  int tmem_cols;
+};
+
+__device__ __forceinline__ int ld_cluster_s32(uint32_t saddr, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(saddr, rank)) : "memory");
+  return v;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(256) w8a8_tile_kernel(W8Args a) {
-  __shared__ int sx[64][17], sw[64][17];
-  const int64_t j0 = static_cast<int64_t>(blockIdx.x) * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int lr = threadIdx.x >> 2, lc = threadIdx.x & 3;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * 64; t0 < a.n_tok;
-       t0 += static_cast<int64_t>(gridDim.y) * 64) {
-    int acc[4][4] = {};
-    for (int k0 = 0; k0 < a.d_in; k0 += 64) {
-      int4 vx = make_int4(0, 0, 0, 0), vw = vx;
-      const int k = k0 + lc * 16;
-      if (k < a.d_in && t0 + lr < a.n_tok)
-        vx = *reinterpret_cast<const int4 *>(a.x + (t0 + lr) * a.d_in + k);
-      if (k < a.d_in && j0 + lr < a.d_out)
-        vw = *reinterpret_cast<const int4 *>(a.w + (j0 + lr) * a.d_in + k);
-      __syncthreads();
-      sx[lr][lc * 4] = vx.x; sx[lr][lc * 4 + 1] = vx.y;
-      sx[lr][lc * 4 + 2] = vx.z; sx[lr][lc * 4 + 3] = vx.w;
-      sw[lr][lc * 4] = vw.x; sw[lr][lc * 4 + 1] = vw.y;
-      sw[lr][lc * 4 + 2] = vw.z; sw[lr][lc * 4 + 3] = vw.w;
-      __syncthreads();
+__global__ void __launch_bounds__(F_THREADS)
+    w8a8_few_kernel(const __grid_constant__ CUtensorMap tmX,
+                    const __grid_constant__ CUtensorMap tmW, W8Args a, FewPlan p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[F_MAX_STAGES], empty[F_MAX_STAGES], acc_full;
+  __shared__ uint32_t tmem_slot;
+  uint8_t *ring = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(blockIdx.x) % p.split;
+  const int tile = static_cast<int>(blockIdx.x) / p.split;
+  const int tt = tile % a.n_tt, jt = tile / a.n_tt;
+  const int stage_bytes = (F_J + p.bn) * PK;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(a.nkb) * rank / p.split);
+  const int nkb = static_cast<int>(static_cast<int64_t>(a.nkb) * (rank + 1) / p.split) - kb0;
+  if (threadIdx.x == 0) {
+    if (blockIdx.x == 0) reset_status(a.status);
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&acc_full, 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, static_cast<uint32_t>(p.tmem_cols));
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  bool ok = true;
+  if (warp == 0 && lane == 0) {
+    int it = 0;
+    for (; it < nkb; ++it) {
+      const int s = it % p.stages, r = it / p.stages;
+      if (!mbar_wait(&empty[s], (r & 1) ^ 1)) { ok = false; break; }
+      uint8_t *st = ring + s * stage_bytes;
+      mbar_arrive_expect_tx(&full[s], stage_bytes);
+      tma_load_2d(st, &tmW, &full[s], (kb0 + it) * PK, jt * F_J);
+      tma_load_2d(st + F_J * PK, &tmX, &full[s], (kb0 + it) * PK, tt * p.bn);
+    }
+    for (int j = it - 1; j >= 0 && j >= it - p.stages; --j)  // the last loads have landed
+      if (!mbar_wait(&full[j % p.stages], (j / p.stages) & 1)) ok = false;
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_s8_s32(F_J, p.bn);
+    for (int it = 0; it < nkb; ++it) {
+      const int s = it % p.stages, r = it / p.stages;
+      if (!mbar_wait(&full[s], r & 1)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t sw = smem_u32(ring + s * stage_bytes), sx = sw + F_J * PK;
 #pragma unroll
-      for (int kk = 0; kk < 16; ++kk) {
-        int xv[4], wv[4];
+      for (int kk = 0; kk < PK / 32; ++kk)
+        mma_s8(tmem, smem_desc_sw128(sw + kk * 32, 16, 1024), smem_desc_sw128(sx + kk * 32, 16, 1024),
+               idesc, (it | kk) != 0);
+      mma_commit(&empty[s]);
+    }
+    mma_commit(&acc_full);
+  }
+  __syncwarp();
+  if (!__all_sync(0xffffffffu, mbar_wait(&acc_full, 0))) ok = false;
+  tc_fence_after();
+
+  const int64_t j = static_cast<int64_t>(jt) * F_J + threadIdx.x;
+  const int64_t t0 = static_cast<int64_t>(tt) * p.bn;
+  const int n = a.n_tok - t0 < p.bn ? static_cast<int>(a.n_tok - t0) : p.bn;
+  const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  const bool live = j < a.d_out;
+  const float ws = live ? __half2float(__ushort_as_half(a.ws[j])) : 0.0f;
+  const int wz = live && a.wz ? a.wz[j] : 0;
+  const float bias = live && a.bias ? a.bias[j] : 0.0f;
+  if (p.split == 1) {
+    for (int c0 = 0; c0 < n; c0 += 32) {
+      float v[32];
+      tmem_ld32(taddr + c0, v);
+      if (live) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          xv[i] = sx[ty + 16 * i][kk];
-          wv[i] = sw[tx + 16 * i][kk];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(xv[i], wv[j], acc[i][j]);
+        for (int i = 0; i < 32; ++i)
+          if (c0 + i < n) finish<T>(a, t0 + c0 + i, j, __float_as_int(v[i]), ws, wz, bias);
       }
     }
+    tc_fence_before();
+    __syncthreads();
+  } else {
+    // every load of this CTA has landed and every MMA has read the ring
+    int *sums = reinterpret_cast<int *>(ring);
+    for (int c0 = 0; c0 < n; c0 += 32) {
+      float v[32];
+      tmem_ld32(taddr + c0, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 32; ++i)
+        if (c0 + i < n) sums[(c0 + i) * F_J + threadIdx.x] = __float_as_int(v[i]);
+    }
+    tc_fence_before();
+    cluster_sync();
+    if (live) {
+      for (int c = rank; c < n; c += p.split) {
+        const uint32_t at = smem_u32(sums + c * F_J + threadIdx.x);
+        int part[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t t = t0 + ty + 16 * i, jj = j0 + tx + 16 * j;
-        if (t < a.n_tok && jj < a.d_out) finish<T>(a, t, jj, acc[i][j]);
+        for (int r = 0; r < 8; ++r) part[r] = r < p.split ? ld_cluster_s32(at, r) : 0;
+        int acc = 0;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) acc += part[r];
+        finish<T>(a, t0 + c, j, acc, ws, wz, bias);
       }
+    }
+    cluster_sync();  // no CTA leaves while another reads its sums
+  }
+  if (!ok) set_status(a.status, kDevTimeout);
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, static_cast<uint32_t>(p.tmem_cols));
   }
 }
 
@@ -489,18 +595,67 @@ gq_status launch_pair(W8Args a, cudaStream_t st) {
   return check_launch("w8a8_pair_kernel");
 }
 
+// Clusters of CTAs per tile: enough of them for two CTAs per SM, each with
+// at least four K steps.  A CTA of a split tile so holds four stages or its
+// share of 108 KB, 72 KB and more: it never shares an SM with a CTA of a
+// kernel that takes all of TMEM (their shared memory is above 190 KB), and
+// at most three of them, 384 columns, share one, so no cluster waits for
+// TMEM columns while it holds some that another cluster waits for.
+FewPlan few_plan(int64_t n_tok, int64_t d_out, int nkb, int &n_tt, int &n_jt) {
+  FewPlan p;
+  n_tt = static_cast<int>((n_tok + F_T - 1) / F_T);
+  const int64_t per = (n_tok + n_tt - 1) / n_tt;
+  p.bn = static_cast<int>((per + 15) / 16 * 16);
+  n_jt = static_cast<int>((d_out + F_J - 1) / F_J);
+  const int64_t tiles = static_cast<int64_t>(n_tt) * n_jt;
+  p.split = 1;
+  while (p.split < 8 && tiles * p.split * 2 <= 2 * num_sms() + num_sms() / 2 && nkb >= 8 * p.split) p.split *= 2;
+  const int stage = (F_J + p.bn) * PK;
+  p.stages = (108 * 1024) / stage;
+  if (p.stages > F_MAX_STAGES) p.stages = F_MAX_STAGES;
+  const int most = (nkb + p.split - 1) / p.split;
+  const int need = p.split > 1 ? (p.bn * F_J * 4 + stage - 1) / stage : 1;
+  if (p.stages > most) p.stages = most > need ? most : need;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < p.bn) p.tmem_cols *= 2;
+  return p;
+}
+
+template <typename T>
+gq_status launch_few(W8Args a, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  a.nkb = (a.d_in + PK - 1) / PK;
+  const FewPlan p = few_plan(a.n_tok, a.d_out, a.nkb, a.n_tt, a.n_jt);
+  CUtensorMap tX, tW;
+  gq_status s = make_tmap_2d(&tX, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.d_in, a.n_tok, a.d_in, PK, p.bn);
+  if (s == GQ_OK)
+    s = make_tmap_2d(&tW, a.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.d_in, a.d_out, a.d_in, PK, F_J);
+  if (s != GQ_OK) return s;
+  const size_t smem = 1024 + static_cast<size_t>(p.stages) * (F_J + p.bn) * PK;
+  allow_smem(w8a8_few_kernel<T>, 1024 + 108 * 1024, done);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.n_tt) * a.n_jt * p.split);
+  cfg.blockDim = dim3(F_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = p.split;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.split > 1 ? 1 : 0;
+  const int slot = timer_begin(GQ_KERNEL_W8A8, st);
+  cudaLaunchKernelEx(&cfg, w8a8_few_kernel<T>, tX, tW, a, p);
+  count_launch();
+  timer_end(slot, st, 2.0 * static_cast<double>(a.n_tok) * a.d_out * a.d_in);
+  return check_launch("w8a8_few_kernel");
+}
+
 template <typename T>
 gq_status launch_typed(W8Args a, cudaStream_t st) {
   a.y_vec = a.d_out * sizeof(T) % 16 == 0;
-  if (a.n_tok > 128) return launch_pair<T>(a, st);
-  const int64_t rows = (a.n_tok + 63) / 64;
-  const dim3 grid(static_cast<unsigned>((a.d_out + 63) / 64),
-                  static_cast<unsigned>(rows < 65535 ? rows : 65535));
-  const int slot = timer_begin(GQ_KERNEL_W8A8, st);
-  w8a8_tile_kernel<T><<<grid, 256, 0, st>>>(a);
-  count_launch();
-  timer_end(slot, st, 2.0 * static_cast<double>(a.n_tok) * a.d_out * a.d_in);
-  return check_launch("w8a8_tile_kernel");
+  if (a.n_tok > 256) return launch_pair<T>(a, st);
+  return launch_few<T>(a, st);
 }
 
 }  // namespace
@@ -510,8 +665,10 @@ gq_status launch_w8a8(const int8_t *w_codes, const uint16_t *w_scales, const int
                       const int32_t *x_sums, int64_t n_tok, const float *bias, int act,
                       const void *M, const void *R, void *Y, gq_dtype y_dtype, int *status,
                       cudaStream_t st) {
-  if (cudaMemsetAsync(status, 0, sizeof(int), st) != cudaSuccess) return check_launch("memset");
-  if (n_tok == 0) return GQ_OK;
+  if (n_tok == 0) {
+    cudaMemsetAsync(status, 0, sizeof(int), st);
+    return check_launch("memset");
+  }
   const W8Args a{w_codes, x_codes, w_scales, w_zpoint, x_scales, x_sums, bias, M, R, Y,
                  d_out,   n_tok,   static_cast<int>(d_in), act, status, 0, 0, 0, 0, 0};
   switch (y_dtype) {
