@@ -110,6 +110,12 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
     if (globaltimer_ns() - t0 > limit_ns) return false;
   }
 }
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -385,6 +391,26 @@ __device__ __forceinline__ float div_by_recip(float a, float b, float r) {
   const float q0 = __fmul_rn(a, r);
   const float e = __fmaf_rn(-q0, b, a);
   return __fmaf_rn(e, r, q0);
+}
+// Pairs of fp32 values on the paired pipe (each half an IEEE operation).
+__device__ __forceinline__ uint64_t f32x2_pack(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f32x2_unpack(uint64_t r, uint32_t &lo, uint32_t &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(r));
+}
+// RN(RN(w / s) + c) for a pair of weights: rs2 = (RN(1/s), RN(1/s)), ns2 = (-s, -s),
+// c2 = (c, c).  The steps of div_by_recip, in pairs.
+__device__ __forceinline__ uint64_t quotient_plus_f32x2(uint64_t w, uint64_t rs2, uint64_t ns2,
+                                                        uint64_t c2) {
+  uint64_t q0, e, q, t;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q0) : "l"(w), "l"(rs2));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q0), "l"(ns2), "l"(w));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(e), "l"(rs2), "l"(q0));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(q), "l"(c2));
+  return t;
 }
 // Integer code of w and its stored nibble, with rs = RN(1 / s).  The
 // quotient is clamped to the code range first (equivalent, since the bounds

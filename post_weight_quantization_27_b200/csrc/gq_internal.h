@@ -50,6 +50,22 @@ gq_status make_tmap_2d(CUtensorMap *map, const void *base, CUtensorMapDataType d
 
 int num_sms();
 
+// Opts one kernel in to its dynamic shared memory, once per device (a static
+// of the function that launches it).
+struct SmemOptIn {
+  std::atomic<uint64_t> done{0};
+  template <typename K>
+  void allow(K kernel, size_t bytes) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(bytes)) == cudaSuccess)
+      done.fetch_or(bit, std::memory_order_relaxed);
+  }
+};
+
 // ---- kernels (each returns GQ_OK or GQ_ERR_CUDA after launching) ----
 // group_size: -1 per row, 0 per tensor (one scale, stored once per row), else per group.
 // bits: 2, 3, 4 or 8 (codes of other widths than 4 need d_in and the group a

@@ -193,25 +193,6 @@ __device__ __forceinline__ uint32_t pack_word(const float (&v)[8], const GridPar
 // half is a base plus its 4-bit code, so the word is sum_j pair_j 16^j minus
 // base * 0x11111111 in 32-bit modular arithmetic (linear, and the codes
 // themselves do not overlap).
-__device__ __forceinline__ uint64_t f32x2_pack(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void f32x2_unpack(uint64_t r, uint32_t &lo, uint32_t &hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(r));
-}
-// RN(RN(w / s) + c) for a pair of weights: rs2 = (RN(1/s), RN(1/s)), ns2 = (-s, -s),
-// c2 = (c, c).  The steps of div_by_recip, in pairs.
-__device__ __forceinline__ uint64_t quotient_plus_f32x2(uint64_t w, uint64_t rs2, uint64_t ns2,
-                                                        uint64_t c2) {
-  uint64_t q0, e, q, t;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q0) : "l"(w), "l"(rs2));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q0), "l"(ns2), "l"(w));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(e), "l"(rs2), "l"(q0));
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(q), "l"(c2));
-  return t;
-}
 __device__ __forceinline__ uint32_t mad_u32(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));

@@ -164,8 +164,9 @@ def _p(t) -> int | None:
 
 
 def _stream(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is None:   # torch.cuda.current_stream().cuda_stream, without the Stream object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None, shape=None) -> torch.Tensor:
@@ -470,13 +471,14 @@ def qlinear_bf16(X: torch.Tensor, d_out: int, q: dict | None = None, W: torch.Te
 ACT8 = dict(ACT, silu=3)
 
 
-def _on_current(t: torch.Tensor, name: str) -> torch.Tensor:
-    """Refuses a tensor of another device than the current one: the launch would go to the current
-    device's stream."""
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return t
+def _arg(t: torch.Tensor, name: str, dtype, shape, dev: int) -> int:
+    """The address of an operand: a dense tensor of this dtype and shape on CUDA device ``dev``, the
+    current one (the launch goes to its stream)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape \
+            or t.get_device() != dev or not t.is_contiguous():
+        _dev(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    return t.data_ptr()
 
 
 def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
@@ -488,15 +490,20 @@ def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     return t
 
 
-def _tokens8(X: torch.Tensor, n_tok: int, d_in: int, with_sums: bool, out, stream):
-    """(codes, scales, sums or None) for n_tok tokens: those of ``out``, checked, or new ones."""
+def _tokens8(X: torch.Tensor, n_tok: int, d_in: int, with_sums: bool, out, stream, dev: int):
+    """The dict of n_tok tokens to be written (that of ``out``, checked, or new tensors) and the
+    addresses of its codes, scales and sums."""
     if out is None:
-        return (_new((n_tok, d_in), torch.int8, X, stream), _new((n_tok,), torch.float32, X, stream),
-                _new((n_tok,), torch.int32, X, stream) if with_sums else None)
-    sums = out.get("sums")
-    return (_on_current(_dev(out["codes"], "codes", torch.int8, (n_tok, d_in)), "codes"),
-            _on_current(_dev(out["scales"], "scales", torch.float32, (n_tok,)), "scales"),
-            None if sums is None else _on_current(_dev(sums, "sums", torch.int32, (n_tok,)), "sums"))
+        codes = _new((n_tok, d_in), torch.int8, X, stream)
+        scales = _new((n_tok,), torch.float32, X, stream)
+        sums = _new((n_tok,), torch.int32, X, stream) if with_sums else None
+        return (dict(codes=codes, scales=scales, sums=sums), codes.data_ptr(), scales.data_ptr(),
+                _p(sums))
+    codes, scales, sums = out["codes"], out["scales"], out.get("sums")
+    return (dict(codes=codes, scales=scales, sums=sums),
+            _arg(codes, "codes", torch.int8, (n_tok, d_in), dev),
+            _arg(scales, "scales", torch.float32, (n_tok,), dev),
+            None if sums is None else _arg(sums, "sums", torch.int32, (n_tok,), dev))
 
 
 def quantize_tokens_int8(X: torch.Tensor, col_mul: torch.Tensor | None = None,
@@ -511,21 +518,22 @@ def quantize_tokens_int8(X: torch.Tensor, col_mul: torch.Tensor | None = None,
     dt = _DTYPES.get(X.dtype)
     if dt is None:
         raise ValueError(f"unsupported X dtype {X.dtype}")
-    _on_current(X, "X")
+    dev = torch._C._cuda_getDevice()
+    if X.get_device() != dev:
+        raise ValueError(f"X is on {X.device}, the current device is cuda:{dev}")
     n_tok, d_in = X.shape
     ldx, one = X.stride()
     if n_tok <= 1:
         ldx = d_in
     if one != 1 and d_in > 1:
         raise ValueError("X's columns must be adjacent")
-    if col_mul is not None:
-        _on_current(_dev(col_mul, "col_mul", torch.float32, (d_in,)), "col_mul")
-    codes, scales, sums = _tokens8(X, n_tok, d_in, with_sums, out, stream)
-    st = lib().gq_quantize_tokens_int8(_p(X), dt, n_tok, d_in, ldx, _p(col_mul), _p(codes),
-                                       _p(scales), _p(sums), _stream(stream))
+    cm = None if col_mul is None else _arg(col_mul, "col_mul", torch.float32, (d_in,), dev)
+    q, codes, scales, sums = _tokens8(X, n_tok, d_in, with_sums, out, stream, dev)
+    st = lib().gq_quantize_tokens_int8(X.data_ptr(), dt, n_tok, d_in, ldx, cm, codes, scales, sums,
+                                       _stream(stream))
     if st:
         _check(st, "gq_quantize_tokens_int8")
-    return dict(codes=codes, scales=scales, sums=sums)
+    return q
 
 
 def rmsnorm_quantize_int8(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
@@ -535,27 +543,31 @@ def rmsnorm_quantize_int8(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e
     as int8 codes with one scale per token.  Returns dict(codes, scales, sums, h): h is the sum,
     written to ``H`` (which may be X or R) or to a new tensor; X itself without R.  ``out`` as for
     quantize_tokens_int8."""
-    _on_current(_dev(X, "X"), "X")
-    dt = _DTYPES.get(X.dtype)
-    if dt is None or X.dim() != 2:
-        raise ValueError(f"X must be [n_tok][d_in] in fp32, fp16 or bf16, got {X.dtype}")
-    n_tok, d_in = X.shape
-    _on_current(_dev(weight, "weight", None, (d_in,)), "weight")
-    if weight.dtype not in _DTYPES:
-        raise ValueError(f"unsupported weight dtype {weight.dtype}")
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError("X must be a CUDA tensor [n_tok][d_in]")
+    xdt = X.dtype
+    dt, wdt = _DTYPES.get(xdt), _DTYPES.get(weight.dtype)
+    if dt is None or wdt is None:
+        raise ValueError(f"X and weight must be fp32, fp16 or bf16, got {xdt} and {weight.dtype}")
+    n_tok, d_in = shape = X.shape
+    dev = torch._C._cuda_getDevice()
+    px = _arg(X, "X", xdt, shape, dev)
+    pw = _arg(weight, "weight", weight.dtype, (d_in,), dev)
+    pr = ph = None
     if R is not None:
-        _on_current(_dev(R, "R", X.dtype, (n_tok, d_in)), "R")
-        H = _new((n_tok, d_in), X.dtype, X, stream) if H is None else \
-            _on_current(_dev(H, "H", X.dtype, (n_tok, d_in)), "H")
+        pr = _arg(R, "R", xdt, shape, dev)
+        if H is None:
+            H = _new(shape, xdt, X, stream)
+        ph = _arg(H, "H", xdt, shape, dev)
     elif H is not None:
         raise ValueError("H is written only with a residual R")
-    codes, scales, sums = _tokens8(X, n_tok, d_in, with_sums, out, stream)
-    st = lib().gq_rmsnorm_quantize_int8(_p(X), _p(R), dt, n_tok, d_in, _p(weight),
-                                        _DTYPES[weight.dtype], eps, _p(H), _p(codes), _p(scales),
-                                        _p(sums), _stream(stream))
+    q, codes, scales, sums = _tokens8(X, n_tok, d_in, with_sums, out, stream, dev)
+    st = lib().gq_rmsnorm_quantize_int8(px, pr, dt, n_tok, d_in, pw, wdt, eps, ph, codes, scales,
+                                        sums, _stream(stream))
     if st:
         _check(st, "gq_rmsnorm_quantize_int8")
-    return dict(codes=codes, scales=scales, sums=sums, h=X if H is None else H)
+    q["h"] = X if H is None else H
+    return q
 
 
 def unpack_int8(q: dict, d_in: int, group_size: int = -1, sym: bool = True, stream=None) -> dict:
@@ -565,13 +577,12 @@ def unpack_int8(q: dict, d_in: int, group_size: int = -1, sym: bool = True, stre
     if group_size not in (-1, 0):
         raise ValueError("an int8 product needs one scale per output channel: group_size -1 or 0")
     bits = int(q.get("bits", 4))
-    qp = _on_current(_dev(q["qpacked"], "qpacked", torch.int32), "qpacked")
+    qp, dev = q["qpacked"], torch._C._cuda_getDevice()
     d_out = qp.shape[0]
-    if tuple(qp.shape) != (d_out, bits * d_in // 32):
-        raise ValueError(f"qpacked must have shape {(d_out, bits * d_in // 32)}, got {tuple(qp.shape)}")
-    _dev(q["scales"], "scales", torch.float16, (d_out, 1))
+    _arg(qp, "qpacked", torch.int32, (d_out, bits * d_in // 32), dev)
+    _arg(q["scales"], "scales", torch.float16, (d_out, 1), dev)
     if not sym:
-        _dev(q["zeros"], "zeros", torch.float16, (d_out, 1))
+        _arg(q["zeros"], "zeros", torch.float16, (d_out, 1), dev)
     codes = _new((d_out, d_in), torch.int8, qp, stream)
     zp = None if sym else _new((d_out,), torch.int32, qp, stream)
     st = lib().gq_unpack_int8(_p(qp), None if sym else _p(q["zeros"]), d_out, d_in, bits,
@@ -593,44 +604,44 @@ def w8a8_matmul(w: dict, x: dict, bias: torch.Tensor | None = None, act: str = "
     bias is fp32 [d_out]; mul and R have Y's shape and dtype (``dtype`` when Y is not given) and may
     be Y itself; act is "none", "relu", "gelu" or "silu"."""
     wc, xc = w["codes"], x["codes"]
-    _on_current(_dev(xc, "x codes", torch.int8), "x codes")
-    _on_current(_dev(wc, "w codes", torch.int8), "w codes")
     n_tok, d_in = xc.shape
     d_out = wc.shape[0]
     if wc.shape[1] != d_in:
         raise ValueError(f"the layer has {wc.shape[1]} inputs, the tokens {d_in}")
-    wsc, xsc, zp, sums = w["scales"], x["scales"], w.get("zpoint"), None
-    _dev(wsc, "w scales", torch.float16)
-    _dev(xsc, "x scales", torch.float32)
-    if wsc.numel() != d_out or xsc.numel() != n_tok:
-        raise ValueError("one scale per output channel and one per token are needed")
+    dev = torch._C._cuda_getDevice()
+    pw = _arg(wc, "w codes", torch.int8, (d_out, d_in), dev)
+    px = _arg(xc, "x codes", torch.int8, (n_tok, d_in), dev)
+    ws_, zp = w["scales"], w.get("zpoint")
+    pws = _arg(ws_, "w scales", torch.float16, (d_out, 1) if ws_.dim() == 2 else (d_out,), dev)
+    pxs = _arg(x["scales"], "x scales", torch.float32, (n_tok,), dev)
+    pz = psum = None
     if zp is not None:
-        _dev(zp, "zpoint", torch.int32, (d_out,))
-        sums = x.get("sums")
-        if sums is None:
+        pz = _arg(zp, "zpoint", torch.int32, (d_out,), dev)
+        if x.get("sums") is None:
             raise ValueError("an affine layer needs the tokens' sums (with_sums=True)")
-        _dev(sums, "sums", torch.int32, (n_tok,))
-    if act not in ACT8:
+        psum = _arg(x["sums"], "sums", torch.int32, (n_tok,), dev)
+    a = ACT8.get(act)
+    if a is None:
         raise ValueError(f"act must be one of {', '.join(ACT8)}")
     shape = (n_tok, d_out)
     if Y is None:
+        if dtype not in _DTYPES:
+            raise ValueError(f"unsupported Y dtype {dtype}")
         Y = _new(shape, dtype, xc, stream)
-    else:
-        _on_current(_dev(Y, "Y", None, shape), "Y")
-    dt = _DTYPES.get(Y.dtype)
+    ydt = Y.dtype
+    dt = _DTYPES.get(ydt)
     if dt is None:
-        raise ValueError(f"unsupported Y dtype {Y.dtype}")
-    if bias is not None:
-        _dev(bias, "bias", torch.float32, (d_out,))
-    if mul is not None:
-        _dev(mul, "mul", Y.dtype, shape)
-    if R is not None:
-        _dev(R, "R", Y.dtype, shape)
+        raise ValueError(f"unsupported Y dtype {ydt}")
     if ws is None:
         ws = _new((256,), torch.uint8, xc, stream)
-    st = lib().gq_w8a8_matmul(_p(wc), _p(wsc), _p(zp), d_out, d_in, _p(xc), _p(xsc), _p(sums), n_tok,
-                              _p(bias), ACT8[act], _p(mul), _p(R), _p(Y), dt, _p(ws), ws.numel(),
-                              _stream(stream))
+    elif ws.get_device() != dev:
+        raise ValueError(f"ws is on {ws.device}, the current device is cuda:{dev}")
+    st = lib().gq_w8a8_matmul(
+        pw, pws, pz, d_out, d_in, px, pxs, psum, n_tok,
+        None if bias is None else _arg(bias, "bias", torch.float32, (d_out,), dev), a,
+        None if mul is None else _arg(mul, "mul", ydt, shape, dev),
+        None if R is None else _arg(R, "R", ydt, shape, dev),
+        _arg(Y, "Y", ydt, shape, dev), dt, ws.data_ptr(), ws.numel(), _stream(stream))
     if st:
         _check(st, "gq_w8a8_matmul")
     return Y
