@@ -6,6 +6,8 @@
 // difference sum x (c - zpoint) at most 128 * 255 * 65536 < 2^31.  One
 // rounding takes it to fp32, where the epilogue works, and one more to the
 // output's type.
+#include <type_traits>
+
 #include "gq_device.cuh"
 #include "gq_internal.h"
 
@@ -36,17 +38,44 @@ __device__ __forceinline__ int sub_wrap(int acc, int z, int xsum) {
                           static_cast<uint32_t>(z) * static_cast<uint32_t>(xsum));
 }
 
-__device__ __forceinline__ float act8(float v, int act) {
-  if (act == GQ_ACT_RELU) return v < 0.0f ? 0.0f : v;   // keeps NaN
-  // v / (1 + e^-w), w = v (SiLU) or 2 u (GELU's tanh form, 0.5 v (1 + tanh
-  // u)).  The intrinsics' few ulps (e^-w: 2 + 1.17 |w|) matter where e^-w is
-  // near 1; where it is large the value itself vanishes.
-  if (act == GQ_ACT_SILU) return __fdividef(v, 1.0f + __expf(-v));
-  if (act == GQ_ACT_GELU) {
-    const float u = 0.7978845608028654f * fmaf(0.044715f * v, v * v, v);
-    return __fdividef(v, 1.0f + __expf(-2.0f * u));
+// SiLU and GELU (tanh form, 0.5 v (1 + tanh u), u = sqrt(2 / pi) (v +
+// 0.044715 v^3)) are v / (1 + 2^t) with t = -v log2 e and t = -2 u log2 e = v
+// (c0 + c1 v^2), two at a time.  The approximate 2^t and reciprocal (a few
+// ulps, and t's rounding) matter where 2^t is near 1; where it is large the
+// value itself vanishes.  NaN stays NaN, in ReLU too.
+__device__ __forceinline__ float over_1_plus_exp2(float v, float t) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return v * r;
+}
+template <int N>
+__device__ __forceinline__ void act_all(float (&v)[N], int act) {
+  static_assert(N % 2 == 0, "pairs");
+  if (act == GQ_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
+  } else if (act == GQ_ACT_SILU) {
+    const uint64_t c = f32x2_pack(-1.4426950408889634f, -1.4426950408889634f);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      uint32_t t0, t1;
+      f32x2_unpack(mul2(f32x2_pack(v[i], v[i + 1]), c), t0, t1);
+      v[i] = over_1_plus_exp2(v[i], __uint_as_float(t0));
+      v[i + 1] = over_1_plus_exp2(v[i + 1], __uint_as_float(t1));
+    }
+  } else if (act == GQ_ACT_GELU) {
+    const uint64_t c0 = f32x2_pack(-2.302208198f, -2.302208198f);    // -2 log2(e) sqrt(2 / pi)
+    const uint64_t c1 = f32x2_pack(-0.1029432396f, -0.1029432396f);  // .. 0.044715
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint64_t p = f32x2_pack(v[i], v[i + 1]);
+      uint32_t t0, t1;
+      f32x2_unpack(mul2(p, fma2(mul2(p, p), c1, c0)), t0, t1);
+      v[i] = over_1_plus_exp2(v[i], __uint_as_float(t0));
+      v[i + 1] = over_1_plus_exp2(v[i + 1], __uint_as_float(t1));
+    }
   }
-  return v;
 }
 
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -61,96 +90,128 @@ __device__ __forceinline__ void from_f(float v, __nv_bfloat16 &o) { o = __float2
 __device__ __forceinline__ void reset_status(int *status) { *reinterpret_cast<volatile int *>(status) = 0; }
 
 // Output j of token t from its integer sum and the output's own scale,
-// zero-point and bias.  The product is taken as (v w_scale) x_scale: |v| <
-// 2^31 times an fp16 scale neither overflows nor loses a normal result.
-template <typename T>
-__device__ __forceinline__ void finish(const W8Args &a, int64_t t, int64_t j, int acc, float ws,
-                                       int wz, float bias) {
-  if (a.wz) acc = sub_wrap(acc, wz, a.xsum[t]);
-  float v = static_cast<float>(acc) * ws * a.xs[t];
-  if (a.bias) v += bias;
-  v = act8(v, a.act);
-  const int64_t i = t * a.d_out + j;
-  if (a.m) v *= to_f(static_cast<const T *>(a.m)[i]);
-  if (a.r) v += to_f(static_cast<const T *>(a.r)[i]);
-  from_f(v, static_cast<T *>(a.y)[i]);
+// zero-point and bias, the token's scale and code sum, and M and R there.
+// The product is taken as (v w_scale) x_scale: |v| < 2^31 times an fp16
+// scale neither overflows nor loses a normal result.
+struct OutCol {
+  uint16_t ws;
+  float bias;
+  int wz;
+  __device__ __forceinline__ float scale() const { return __half2float(__ushort_as_half(ws)); }
+};
+__device__ __forceinline__ OutCol out_col(const W8Args &a, int64_t j, bool live) {
+  OutCol o;
+  o.ws = live ? a.ws[j] : 0;
+  o.wz = live && a.wz ? a.wz[j] : 0;
+  o.bias = live && a.bias ? a.bias[j] : 0.0f;
+  return o;
+}
+__device__ __forceinline__ float finish(const W8Args &a, const OutCol &o, int acc, float xs,
+                                        int xsum, float m, float r) {
+  if (a.wz) acc = sub_wrap(acc, o.wz, xsum);
+  float v[2] = {static_cast<float>(acc) * o.scale() * xs, 0.0f};
+  if (a.bias) v[0] += o.bias;
+  act_all(v, a.act);
+  if (a.m) v[0] *= m;
+  if (a.r) v[0] += r;
+  return v[0];
 }
 
 // ---------------------------------------------------------------- 32 outputs of a token
-// v = the raw integer sums (as bits) -> x_scale w_scale (acc - z xsum) + bias.
+__device__ __forceinline__ uint64_t int2float2(float a, float b) {  // of integers held as bits
+  return f32x2_pack(static_cast<float>(__float_as_int(a)), static_cast<float>(__float_as_int(b)));
+}
+// v = the raw integer sums (as bits) -> x_scale w_scale (acc - z xsum) +
+// bias, from the columns' operands in shared memory.  (Each option loops
+// over all columns by itself: a branch per column would keep the compiler
+// from interleaving them.)
 __device__ __forceinline__ void scale32(const W8Args &a, const float *s, const int *z,
                                         const float *b, float xs, int xsum, float (&v)[32]) {
+  if (a.wz) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    const float4 s4 = *reinterpret_cast<const float4 *>(s + i);
-    const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
-    int zv[4] = {0, 0, 0, 0};
-    float bv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (a.wz) {
+    for (int i = 0; i < 32; i += 4) {
       const int4 z4 = *reinterpret_cast<const int4 *>(z + i);
-      zv[0] = z4.x; zv[1] = z4.y; zv[2] = z4.z; zv[3] = z4.w;
-    }
-    if (a.bias) {
-      const float4 b4 = *reinterpret_cast<const float4 *>(b + i);
-      bv[0] = b4.x; bv[1] = b4.y; bv[2] = b4.z; bv[3] = b4.w;
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      int acc = __float_as_int(v[i + e]);
-      if (a.wz) acc = sub_wrap(acc, zv[e], xsum);
-      v[i + e] = static_cast<float>(acc) * sv[e] * xs;
-      if (a.bias) v[i + e] += bv[e];
+      v[i] = __int_as_float(sub_wrap(__float_as_int(v[i]), z4.x, xsum));
+      v[i + 1] = __int_as_float(sub_wrap(__float_as_int(v[i + 1]), z4.y, xsum));
+      v[i + 2] = __int_as_float(sub_wrap(__float_as_int(v[i + 2]), z4.z, xsum));
+      v[i + 3] = __int_as_float(sub_wrap(__float_as_int(v[i + 3]), z4.w, xsum));
     }
   }
-}
-__device__ __forceinline__ void act32(float (&v)[32], int act) {
-  if (act == GQ_ACT_NONE) return;
+  const uint64_t xs2 = f32x2_pack(xs, xs);
+  uint64_t p[16];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = act8(v[i], act);
+  for (int i = 0; i < 16; i += 2) {
+    const ulonglong2 s4 = *reinterpret_cast<const ulonglong2 *>(s + 2 * i);
+    p[i] = mul2(mul2(int2float2(v[2 * i], v[2 * i + 1]), s4.x), xs2);
+    p[i + 1] = mul2(mul2(int2float2(v[2 * i + 2], v[2 * i + 3]), s4.y), xs2);
+  }
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const ulonglong2 b4 = *reinterpret_cast<const ulonglong2 *>(b + 2 * i);
+      p[i] = add2(p[i], b4.x);
+      p[i + 1] = add2(p[i + 1], b4.y);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    uint32_t lo, hi;
+    f32x2_unpack(p[i], lo, hi);
+    v[2 * i] = __uint_as_float(lo);
+    v[2 * i + 1] = __uint_as_float(hi);
+  }
 }
-// v = v * M + R for outputs j .. j + 31 of a token; the rows are read 16
-// bytes at a time where they are a multiple of 16 bytes long.
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+// M or R over a box of 32 tokens x BC = 64 / sizeof(T) outputs: four lanes
+// take a row's 64 bytes (a lane per row would touch 32 lines an instruction:
+// 2560 x 2048 x 8192 with a residual 51 against 40 us), and the rows change
+// hands in the warp's staging buffer, laid out as the boxes that leave by it.
+__device__ __forceinline__ int box_at(int r, int c) {   // 16-byte chunk c of row r
+  return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
 template <typename T>
-__device__ __forceinline__ void load32(const W8Args &a, const T *p, int64_t j, float (&f)[32]) {
-  constexpr int E = 16 / sizeof(T);
-  if (a.y_vec) {
+struct Box {
+  static constexpr int E = 16 / static_cast<int>(sizeof(T));
+  uint4 u[4];
+  __device__ __forceinline__ void load(const W8Args &a, const void *base, int64_t row0, int64_t j0,
+                                       int lane) {
+    const int64_t j = j0 + (lane & 3) * E;
+    const T *p = static_cast<const T *>(base) + (row0 + (lane >> 2)) * a.d_out + j;
 #pragma unroll
-    for (int i = 0; i < 32; i += E) {
-      uint4 u = make_uint4(0u, 0u, 0u, 0u);
-      if (j + i < a.d_out) u = *reinterpret_cast<const uint4 *>(p + i);
-      const T *e = reinterpret_cast<const T *>(&u);
+    for (int i = 0; i < 4; ++i, p += 8 * a.d_out) {
+      if (row0 + (lane >> 2) + 8 * i >= a.n_tok) break;
+      if (a.y_vec) {
+        if (j < a.d_out) u[i] = *reinterpret_cast<const uint4 *>(p);
+      } else {
 #pragma unroll
-      for (int k = 0; k < E; ++k) f[i + k] = to_f(e[k]);
+        for (int e = 0; e < E; ++e)
+          if (j + e < a.d_out) reinterpret_cast<T *>(&u[i])[e] = p[e];
+      }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] = j + i < a.d_out ? to_f(p[i]) : 0.0f;
   }
-}
-template <typename T>
-__device__ __forceinline__ void mul_add32(const W8Args &a, int64_t row, int64_t j, float (&v)[32]) {
-  const int64_t at = row * a.d_out + j;
-  if (a.m) {
-    float f[32];
-    load32<T>(a, static_cast<const T *>(a.m) + at, j, f);
+  // This lane's row of the box, in place of what it loaded.
+  __device__ __forceinline__ void to_row(uint8_t *stg, int lane) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] *= f[i];
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4 *>(stg + box_at((lane >> 2) + 8 * i, lane & 3)) = u[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const uint4 *>(stg + box_at(lane, i));
+    __syncwarp();
   }
-  if (a.r) {
-    float f[32];
-    load32<T>(a, static_cast<const T *>(a.r) + at, j, f);
+  template <int H>
+  __device__ __forceinline__ void times(float (&v)[32]) const {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] += f[i];
+    for (int i = 0; i < 4 * E; ++i) v[H * 4 * E + i] *= to_f(reinterpret_cast<const T *>(u)[i]);
   }
-}
-// 32 values rounded to T into this lane's row of a 32-row box of 128-byte
-// rows (16-byte chunk c of row r at c ^ (r % 8)).
-__device__ __forceinline__ void stage32(uint8_t *row, int r, int, const float (&v)[32], float) {
+  template <int H>
+  __device__ __forceinline__ void plus(float (&v)[32]) const {
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<float4 *>(row + ((c ^ (r & 7)) << 4)) =
-        make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-}
+    for (int i = 0; i < 4 * E; ++i) v[H * 4 * E + i] += to_f(reinterpret_cast<const T *>(u)[i]);
+  }
+};
 __device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&h);
@@ -159,8 +220,19 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-template <typename T>
-__device__ __forceinline__ void stage32(uint8_t *row, int r, int sub, const float (&v)[32], T t) {
+// The values v[H BC ..] of a token, BC = 64 / sizeof(T) of them, rounded to T
+// into this lane's row of a box of 32 rows of 64 bytes (16-byte chunk c of
+// row r at c ^ (r / 2 % 4): the tensor map's 64-byte swizzle, and no bank
+// conflicts).
+template <int H>
+__device__ __forceinline__ void stage_row(uint8_t *stg, int r, const float (&v)[32], float) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<float4 *>(stg + box_at(r, c)) =
+        make_float4(v[16 * H + 4 * c], v[16 * H + 4 * c + 1], v[16 * H + 4 * c + 2], v[16 * H + 4 * c + 3]);
+}
+template <int H, typename T>
+__device__ __forceinline__ void stage_row(uint8_t *stg, int r, const float (&v)[32], T t) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     uint4 u;
@@ -168,51 +240,63 @@ __device__ __forceinline__ void stage32(uint8_t *row, int r, int sub, const floa
     u.y = pack2(v[8 * c + 2], v[8 * c + 3], t);
     u.z = pack2(v[8 * c + 4], v[8 * c + 5], t);
     u.w = pack2(v[8 * c + 6], v[8 * c + 7], t);
-    *reinterpret_cast<uint4 *>(row + (((4 * sub + c) ^ (r & 7)) << 4)) = u;
+    *reinterpret_cast<uint4 *>(stg + box_at(r, c)) = u;
   }
 }
-// A staged box to Y with ordinary stores, a row at a time.
+// A staged box to Y with ordinary stores: half a row (16-bit: a row) per
+// 16 (32) lanes.
 template <typename T>
 __device__ __forceinline__ void store_box(const W8Args &a, const uint8_t *stg, int lane,
                                           int64_t row0, int64_t j0) {
-  constexpr int CC = 128 / sizeof(T), E = 16 / sizeof(T);
-  T *y = static_cast<T *>(a.y) + row0 * a.d_out + j0;
+  constexpr int BC = 64 / sizeof(T), E = 16 / sizeof(T), RS = 32 / BC;   // rows per step
+  const int c = lane % BC;
+  T *y = static_cast<T *>(a.y) + row0 * a.d_out + j0 + c;
   const int rows = a.n_tok - row0 < 32 ? static_cast<int>(a.n_tok - row0) : 32;
-  for (int r = 0; r < rows; ++r) {
-#pragma unroll
-    for (int c = lane; c < CC; c += 32)
-      if (j0 + c < a.d_out)
-        y[r * a.d_out + c] = *reinterpret_cast<const T *>(stg + r * 128 + (((c / E) ^ (r & 7)) << 4) +
-                                                          (c % E) * sizeof(T));
-  }
+  if (j0 + c >= a.d_out) return;
+  for (int r = lane / BC; r < rows; r += RS)
+    y[r * a.d_out] = *reinterpret_cast<const T *>(stg + box_at(r, c / E) + (c % E) * sizeof(T));
 }
 
 // ---------------------------------------------------------------- many tokens
-// 256 (tokens) x 256 (outputs) tiles on CTA pairs (tcgen05 cta_group::2,
-// kind::i8), persistent, K in steps of 128 bytes:
+// 256 (tokens) x PJ = 256 or 128 (outputs) tiles on CTA pairs (tcgen05
+// cta_group::2, kind::i8), persistent, K in steps of 128 bytes:
 //   warp 0      TMA: CTA r of the pair stages the tile's token rows 128 r ..
-//               and output rows 128 r .., both CTAs' loads completing on CTA
-//               0's full[s] (64 KB a stage)
-//   warp 1      CTA 0: four MMAs of M = N = 256, K = 32 a stage into one of
-//               two 256-column TMEM accumulators; each CTA receives its 128
+//               and output rows PJ / 2 r .., both CTAs' loads completing on
+//               CTA 0's full[s]
+//   warp 1      CTA 0: four MMAs of M = 256, N = PJ, K = 32 a stage into one
+//               of two PJ-column TMEM accumulators; each CTA receives its 128
 //               tokens' rows
-//   warps 2-9   epilogue: a thread owns a token, a warp 32 tokens x 128
-//               outputs; the columns' scales, zero-points and bias come once
-//               per tile through shared memory; results pass a 128-byte-
-//               swizzled buffer of the warp's own and leave by TMA store
-//               (by coalesced stores where Y's rows are no multiple of 16
-//               bytes).
-constexpr int PT = 256, PJ = 256, PK = 128, P_STAGES = 5;
-constexpr int P_TILE_BYTES = 128 * PK;                 // one operand of one CTA: 16 KB
-constexpr int P_STAGE_BYTES = 2 * P_TILE_BYTES;
-constexpr int P_STAGING = 4096;                        // per epilogue warp: 32 rows x 128 bytes
-constexpr int P_THREADS = 320;
-constexpr size_t P_SMEM = 1024 + P_STAGES * P_STAGE_BYTES + 8 * P_STAGING + 2 * PJ * 12 + 256;
+//   the others  epilogue, a warp per 32 tokens x 64 outputs, a thread per
+//               token: the columns' scales, zero-points and bias come once
+//               per tile through shared memory, loaded a tile ahead; results
+//               pass a 64-byte-swizzled buffer of the warp's own and leave
+//               by TMA store (by coalesced stores where Y's rows are no
+//               multiple of 16 bytes).
+constexpr int PT = 256, PK = 128;
+constexpr int P_STAGING = 2048;                        // per epilogue warp: 32 rows x 64 bytes
 
+template <int PJ>
+struct PairShape {
+  static constexpr int kStages = PJ == 256 ? 5 : 7;
+  static constexpr int kX = 128 * PK, kW = PJ / 2 * PK;  // one CTA's operands of a stage
+  static constexpr int kStage = kX + kW;
+  static constexpr int kWarps = PJ / 16;                 // of the epilogue
+  static constexpr int kCols = 64;                       // outputs of each of its warps
+  static constexpr int kThreads = 64 + 32 * kWarps;
+  static constexpr size_t kSmem = 1024 + kStages * kStage + kWarps * P_STAGING + 2 * PJ * 12 + 256;
+};
+
+template <int PJ>
 struct Cols {              // per-output operands of a tile, in shared memory
   float s[PJ];
   int z[PJ];
   float b[PJ];
+};
+struct TileOps {           // what one thread brings for a tile: a column's and its token's
+  uint16_t ws;
+  int wz;
+  float bias, xs;
+  int xsum;
 };
 
 // Tile t -> (token tile, output tile) in groups of 8 token tiles, so that the
@@ -225,24 +309,26 @@ __device__ __forceinline__ void pair_tile(int t, int n_tt, int n_jt, int &tt, in
   jt = r / rows;
 }
 
-template <typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
+template <typename T, int PJ>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<PJ>::kThreads, 1)
     w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX,
                      const __grid_constant__ CUtensorMap tmW,
                      const __grid_constant__ CUtensorMap tmY, W8Args a) {
+  using S = PairShape<PJ>;
+  constexpr int P_STAGES = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t *staging = smem + P_STAGES * P_STAGE_BYTES;
-  Cols *cols = reinterpret_cast<Cols *>(staging + 8 * P_STAGING);
+  uint8_t *staging = smem + P_STAGES * S::kStage;
+  Cols<PJ> *cols = reinterpret_cast<Cols<PJ> *>(staging + S::kWarps * P_STAGING);
   uint64_t *full = reinterpret_cast<uint64_t *>(cols + 2);  // CTA 0: both CTAs' loads landed
   uint64_t *empty = full + P_STAGES;                        // per CTA: MMAs done with the stage
   uint64_t *acc_full = empty + P_STAGES;                    // per CTA
-  uint64_t *acc_empty = acc_full + 2;                       // CTA 0: 16 epilogue warps
+  uint64_t *acc_empty = acc_full + 2;                       // CTA 0: both CTAs' epilogue warps
   uint64_t *drain = acc_empty + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = static_cast<int>(blockIdx.x >> 1), n_pairs = static_cast<int>(gridDim.x >> 1);
   const int n_tiles = a.n_tt * a.n_jt;
@@ -254,7 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 16);
+      mbar_init(&acc_empty[b], 2 * S::kWarps);
     }
     mbar_init(drain, 1);
     fence_barrier_init();
@@ -262,134 +348,198 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
     tma_prefetch_desc(&tmW);
   }
   if (warp == 1) {
-    tmem_alloc_pair(tmem_slot, 512);
+    tmem_alloc_pair(tmem_slot, 2 * PJ);
     tmem_relinquish_pair();
   }
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int half0 = static_cast<int>(rank) * 128;  // this CTA's token and output rows in a tile
+  const int half0 = static_cast<int>(rank) * 128;  // this CTA's token rows in a tile
 
   if (warp == 0) {
-    if (lane == 0) {
-      bool ok = true;
-      uint32_t it = 0;
-      for (int t = pair; t < n_tiles && ok; t += n_pairs) {
-        int tt, jt;
-        pair_tile(t, a.n_tt, a.n_jt, tt, jt);
-        for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-          const uint32_t s = it % P_STAGES, r = it / P_STAGES;
-          if (!mbar_wait(&empty[s], (r & 1) ^ 1)) { ok = false; break; }
-          uint8_t *st = smem + s * P_STAGE_BYTES;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * P_STAGE_BYTES);
-          tma_load_2d_pair(st, &tmX, &full[s], kb * PK, tt * PT + half0);
-          tma_load_2d_pair(st + P_TILE_BYTES, &tmW, &full[s], kb * PK, jt * PJ + half0);
+    // (The two issuing warps share their schedulers with the epilogue's: all
+    // their lanes walk the loop, so that its values stay in uniform registers
+    // and a step is few instructions; one lane issues.)
+    const bool leader = elect_one();
+    bool ok = true;
+    uint32_t s = 0, ph = 1, done = 0;
+    const uint32_t base = smem_u32(smem), full0 = mapa_shared(smem_u32(full), 0);
+    for (int t = pair; t < n_tiles && ok; t += n_pairs) {
+      int tt, jt;
+      pair_tile(t, a.n_tt, a.n_jt, tt, jt);
+      const int yx = tt * PT + half0, yw = jt * PJ + static_cast<int>(rank) * (PJ / 2);
+      for (int kb = 0; kb < a.nkb; ++kb) {
+        if (!mbar_wait_warp(&empty[s], ph)) { ok = false; break; }
+        if (leader) {
+          const uint32_t st = base + s * S::kStage;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kStage);
+          tma_load_2d_pair(st, &tmX, full0 + 8 * s, kb * PK, yx);
+          tma_load_2d_pair(st + S::kX, &tmW, full0 + 8 * s, kb * PK, yw);
+        }
+        done |= 1u << s;
+        if (++s == P_STAGES) {
+          s = 0;
+          ph ^= 1;
         }
       }
-      if (rank == 0) {  // the last loads of both CTAs have landed
-        const uint32_t n_wait = it < P_STAGES ? it : P_STAGES;
-        for (uint32_t k = 0; k < n_wait; ++k) {
-          const uint32_t j = it - 1 - k;
-          if (!mbar_wait(&full[j % P_STAGES], (j / P_STAGES) & 1)) ok = false;
-        }
-      }
-      if (!ok) set_status(a.status, kDevTimeout);
     }
+    if (rank == 0) {  // the last loads of both CTAs have landed: stage q's was in this or the last lap
+      for (uint32_t q = 0; q < P_STAGES; ++q)
+        if ((done >> q & 1) && !mbar_wait_warp(&full[q], q < s ? ph ^ 1 : ph)) ok = false;
+    }
+    if (!ok && leader) set_status(a.status, kDevTimeout);
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool leader = elect_one();
       bool ok = true;
-      uint32_t it = 0, ch = 0;
+      uint32_t s = 0, ph = 0, ch = 0;
       constexpr uint32_t idesc = idesc_s8_s32(PT, PJ);
+      const uint64_t dx0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t dw0 = smem_desc_sw128(smem_u32(smem) + S::kX, 16, 1024);
       for (int t = pair; t < n_tiles && ok; t += n_pairs, ++ch) {
         const uint32_t buf = ch & 1, use = ch >> 1;
-        if (!mbar_wait_cluster(&acc_empty[buf], (use & 1) ^ 1)) { ok = false; break; }
+        if (!mbar_wait_cluster_warp(&acc_empty[buf], (use & 1) ^ 1)) { ok = false; break; }
         tc_fence_after();
-        for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-          const uint32_t s = it % P_STAGES, r = it / P_STAGES;
-          if (!mbar_wait_cluster(&full[s], r & 1)) { ok = false; break; }
+        const uint32_t acc = tmem + buf * PJ;
+        for (int kb = 0; kb < a.nkb; ++kb) {
+          if (!mbar_wait_cluster_warp(&full[s], ph)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sx = smem_u32(smem + s * P_STAGE_BYTES), sw = sx + P_TILE_BYTES;
+          if (leader) {
+            const uint64_t dx = dx0 + s * (S::kStage >> 4), dw = dw0 + s * (S::kStage >> 4);
+            mma_s8_pair(acc, dx, dw, idesc, kb != 0);
 #pragma unroll
-          for (int kk = 0; kk < PK / 32; ++kk)
-            mma_s8_pair(tmem + buf * PJ, smem_desc_sw128(sx + kk * 32, 16, 1024),
-                        smem_desc_sw128(sw + kk * 32, 16, 1024), idesc, (kb | kk) != 0);
-          mma_commit_pair(&empty[s], 3);
+            for (int kk = 1; kk < PK / 32; ++kk) mma_s8_pair(acc, dx + 2 * kk, dw + 2 * kk, idesc, 1u);
+            mma_commit_pair(&empty[s], 3);
+          }
+          if (++s == P_STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
         }
         if (!ok) break;
-        mma_commit_pair(&acc_full[buf], 3);
+        if (leader) mma_commit_pair(&acc_full[buf], 3);
       }
-      mma_commit_pair(drain, 1);
-      if (!mbar_wait(drain, 0)) ok = false;
-      if (!ok) set_status(a.status, kDevTimeout);
+      if (leader) mma_commit_pair(drain, 1);
+      if (!mbar_wait_warp(drain, 0)) ok = false;
+      if (!ok && leader) set_status(a.status, kDevTimeout);
     }
   } else {
-    constexpr int CC = 128 / sizeof(T);           // outputs per staged box
-    const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;
+    constexpr int BC = 64 / sizeof(T);            // outputs per staged box
+    const int ew = warp - 2, quarter = warp & 3, col0 = (ew >> 2) * S::kCols, c = threadIdx.x - 64;
     uint8_t *stg = staging + ew * P_STAGING;
-    uint8_t *stg_row = stg + lane * 128;
+    auto load_ops = [&](int t) {
+      TileOps o{};
+      if (t >= n_tiles) return o;
+      int tt, jt;
+      pair_tile(t, a.n_tt, a.n_jt, tt, jt);
+      const int64_t j = static_cast<int64_t>(jt) * PJ + c;
+      if (c < PJ && j < a.d_out) {
+        o.ws = a.ws[j];
+        if (a.wz) o.wz = a.wz[j];
+        if (a.bias) o.bias = a.bias[j];
+      }
+      const int64_t row = static_cast<int64_t>(tt) * PT + half0 + quarter * 32 + lane;
+      if (row < a.n_tok) {
+        o.xs = a.xs[row];
+        if (a.wz) o.xsum = a.xsum[row];
+      }
+      return o;
+    };
+    TileOps next = load_ops(pair);
     uint32_t ch = 0;
     bool ok = true;
     for (int t = pair; t < n_tiles; t += n_pairs, ++ch) {
       int tt, jt;
       pair_tile(t, a.n_tt, a.n_jt, tt, jt);
       const uint32_t buf = ch & 1, use = ch >> 1;
-      Cols &cl = cols[buf];
-      {
-        // the other buffer may still be read: this one was last read before
-        // every warp passed the previous tile's barrier
-        const int c = threadIdx.x - 64;
-        const int64_t j = static_cast<int64_t>(jt) * PJ + c;
-        const bool in = j < a.d_out;
-        cl.s[c] = in ? __half2float(__ushort_as_half(a.ws[j])) : 0.0f;
-        cl.z[c] = in && a.wz ? a.wz[j] : 0;
-        cl.b[c] = in && a.bias ? a.bias[j] : 0.0f;
+      const TileOps ops = next;
+      Cols<PJ> &cl = cols[buf];
+      if (c < PJ) {
+        // (the other buffer may still be read: this one was last read before
+        // every warp passed the previous tile's barrier)
+        cl.s[c] = __half2float(__ushort_as_half(ops.ws));
+        cl.z[c] = ops.wz;
+        cl.b[c] = ops.bias;
       }
+      next = load_ops(t + n_pairs);
       const int64_t row0 = static_cast<int64_t>(tt) * PT + half0 + quarter * 32;
-      const int64_t row = row0 + lane;
-      const bool live = row < a.n_tok;
-      const float xs = live ? a.xs[row] : 0.0f;
-      const int xsum = live && a.wz ? a.xsum[row] : 0;
-      named_bar_sync(1, 256);
+      // M and R: the next tile's go to L2 now; this tile's, 16-bit, come
+      // before the sums are needed, fp32, twice the registers, when they are
+      constexpr bool kEarly = sizeof(T) == 2;
+      Box<T> m, r;
+      auto load_mr = [&](int64_t j) {
+        if (a.m) m.load(a, a.m, row0, j, lane);
+        if (a.r) r.load(a, a.r, row0, j, lane);
+      };
+      if (a.m || a.r) {
+        if (kEarly) load_mr(static_cast<int64_t>(jt) * PJ + col0);
+        if (t + n_pairs < n_tiles) {
+          int t2, j2;
+          pair_tile(t + n_pairs, a.n_tt, a.n_jt, t2, j2);
+          const int64_t next_row = static_cast<int64_t>(t2) * PT + half0 + quarter * 32 + lane;
+          const int64_t jw = static_cast<int64_t>(j2) * PJ + col0;
+          for (int64_t j = jw; next_row < a.n_tok && j < jw + S::kCols && j < a.d_out; j += 128 / sizeof(T)) {
+            if (a.m) prefetch_l2(static_cast<const T *>(a.m) + next_row * a.d_out + j);
+            if (a.r) prefetch_l2(static_cast<const T *>(a.r) + next_row * a.d_out + j);
+          }
+        }
+      }
+      named_bar_sync(1, 32 * S::kWarps);
       // (a warp whose wait gave up keeps meeting the others at the barrier)
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], use & 1));
       if (!ok) continue;
       tc_fence_after();
-      const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * PJ + half * 128;
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * PJ + col0;
+      // (rolled: the options' code per 32 columns is large, and the warps
+      // would wait for instructions)
 #pragma unroll 1
-      for (int b = 0; b < 128 / CC; ++b) {
-        const int c0 = half * 128 + b * CC;                       // column in the tile
-        const int64_t j0 = static_cast<int64_t>(jt) * PJ + c0;
-        if (a.y_tma) {
-          if (lane == 0) bulk_wait_group_read0();
-          __syncwarp();
-        }
-#pragma unroll
-        for (int sub = 0; sub < CC / 32; ++sub) {
-          float v[32];
-          tmem_ld32(taddr + b * CC + sub * 32, v);
-          scale32(a, cl.s + c0 + sub * 32, cl.z + c0 + sub * 32, cl.b + c0 + sub * 32, xs, xsum, v);
-          act32(v, a.act);
-          if (live) mul_add32<T>(a, row, j0 + sub * 32, v);
-          stage32(stg_row, lane, sub, v, T());
-        }
-        if (b == 128 / CC - 1) {
+      for (int q = 0; q < S::kCols / 32; ++q) {
+        const int cq = col0 + q * 32;                              // column in the tile
+        const int64_t j0 = static_cast<int64_t>(jt) * PJ + cq;
+        float v[32];
+        tmem_ld32(taddr + q * 32, v);
+        if (q == S::kCols / 32 - 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(&acc_empty[buf], 0);
         }
-        if (a.y_tma) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && j0 < a.d_out && row0 < a.n_tok) {
-            tma_store_2d(&tmY, stg, static_cast<int32_t>(j0), static_cast<int32_t>(row0));
-            bulk_commit_group();
+        scale32(a, cl.s + cq, cl.z + cq, cl.b + cq, ops.xs, ops.xsum, v);
+        act_all(v, a.act);
+        auto box = [&](auto half) {
+          constexpr int H = decltype(half)::value;
+          const int64_t jb = j0 + H * BC;
+          if (a.y_tma) {
+            if (lane == 0) bulk_wait_group_read0();                // the buffer's last box has left it
+            __syncwarp();
           }
-        } else {
-          __syncwarp();
-          store_box<T>(a, stg, lane, row0, j0);
-          __syncwarp();
-        }
+          if (a.m) {
+            if (!kEarly) m.load(a, a.m, row0, jb, lane);
+            m.to_row(stg, lane);
+            m.template times<H>(v);
+          }
+          if (a.r) {
+            if (!kEarly) r.load(a, a.r, row0, jb, lane);
+            r.to_row(stg, lane);
+            r.template plus<H>(v);
+          }
+          if (kEarly && q + 1 < S::kCols / 32) load_mr(j0 + 32);
+          stage_row<H>(stg, lane, v, T());
+          if (a.y_tma) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && jb < a.d_out && row0 < a.n_tok) {
+              tma_store_2d(&tmY, stg, static_cast<int32_t>(jb), static_cast<int32_t>(row0));
+              bulk_commit_group();
+            }
+          } else {
+            __syncwarp();
+            store_box<T>(a, stg, lane, row0, jb);
+            __syncwarp();
+          }
+        };
+        box(std::integral_constant<int, 0>());
+        if constexpr (BC == 16) box(std::integral_constant<int, 1>());
       }
     }
     if (lane == 0) bulk_wait_group0();
@@ -404,7 +554,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
+    tmem_dealloc_pair(tmem, 2 * PJ);
   }
 }
 
@@ -419,18 +569,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
 // additions does not matter, no workspace and no second launch.
 // A lane owns an output, so a warp's accesses to Y, M and R are contiguous
 // whatever d_out is.
-constexpr int F_J = 128, F_T = 128, F_MAX_STAGES = 8, F_THREADS = 128;
+constexpr int F_J = 128, F_T = 128, F_MAX_STAGES = 12, F_THREADS = 128;
 
 struct FewPlan {
   int bn;            // tokens per tile, a multiple of 16
   int stages, split;
   int tmem_cols;
+  int steps;         // K steps on the fullest SM
 };
 
-__device__ __forceinline__ int ld_cluster_s32(uint32_t saddr, uint32_t rank) {
+__device__ __forceinline__ int ld_cluster_s32(uint32_t cluster_addr) {
   int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(saddr, rank)) : "memory");
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
   return v;
+}
+
+// The token columns c0, c0 + step, .. (NC of them, those below n) of output
+// j, in stages over all of them: a warp is alone on its scheduler here, and
+// one column after another would wait for each instruction in turn (128
+// columns: 17.5 -> 10 us at 768 -> 2304).
+template <typename T, int NC>
+__device__ __forceinline__ void few_columns(const W8Args &a, const OutCol &o, bool live, int64_t t0,
+                                            int c0, int step, int n, int64_t j, const float *xs,
+                                            const int *xsum, int (&acc)[NC]) {
+  const int64_t at = (t0 + c0) * a.d_out + j, pitch = a.d_out * step;
+  T mv[NC], rv[NC];
+  if (a.m) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (live && c0 + i * step < n) mv[i] = static_cast<const T *>(a.m)[at + i * pitch];
+  }
+  if (a.r) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (live && c0 + i * step < n) rv[i] = static_cast<const T *>(a.r)[at + i * pitch];
+  }
+  if (a.wz) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (c0 + i * step < n) acc[i] = sub_wrap(acc[i], o.wz, xsum[c0 + i * step]);
+  }
+  float v[NC];
+  const float ws = o.scale();
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+    v[i] = c0 + i * step < n ? static_cast<float>(acc[i]) * ws * xs[c0 + i * step] : 0.0f;
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) v[i] += o.bias;
+  }
+  act_all(v, a.act);
+  if (a.m) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) v[i] *= to_f(mv[i]);
+  }
+  if (a.r) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) v[i] += to_f(rv[i]);
+  }
+  if (!live) return;
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+    if (c0 + i * step < n) from_f(v[i], static_cast<T *>(a.y)[at + i * pitch]);
 }
 
 template <typename T>
@@ -440,9 +640,11 @@ __global__ void __launch_bounds__(F_THREADS)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[F_MAX_STAGES], empty[F_MAX_STAGES], acc_full;
   __shared__ uint32_t tmem_slot;
+  __shared__ float xs[F_T];
+  __shared__ int xsum[F_T];
   uint8_t *ring = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int rank = static_cast<int>(blockIdx.x) % p.split;
   const int tile = static_cast<int>(blockIdx.x) / p.split;
   const int tt = tile % a.n_tt, jt = tile / a.n_tt;
@@ -464,60 +666,87 @@ __global__ void __launch_bounds__(F_THREADS)
     tmem_alloc(&tmem_slot, static_cast<uint32_t>(p.tmem_cols));
     tmem_relinquish();
   }
+  // the epilogue's operands of this output, on their way while the tiles are
+  const int64_t j = static_cast<int64_t>(jt) * F_J + threadIdx.x;
+  const int64_t t0 = static_cast<int64_t>(tt) * p.bn;
+  const int n = a.n_tok - t0 < p.bn ? static_cast<int>(a.n_tok - t0) : p.bn;
+  const bool live = j < a.d_out;
+  const OutCol o = out_col(a, j, live);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
   bool ok = true;
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
+    const bool leader = elect_one();
+    const uint32_t base = smem_u32(ring);
+    int s = 0;
+    uint32_t ph = 1;
     int it = 0;
     for (; it < nkb; ++it) {
-      const int s = it % p.stages, r = it / p.stages;
-      if (!mbar_wait(&empty[s], (r & 1) ^ 1)) { ok = false; break; }
-      uint8_t *st = ring + s * stage_bytes;
-      mbar_arrive_expect_tx(&full[s], stage_bytes);
-      tma_load_2d(st, &tmW, &full[s], (kb0 + it) * PK, jt * F_J);
-      tma_load_2d(st + F_J * PK, &tmX, &full[s], (kb0 + it) * PK, tt * p.bn);
+      if (!mbar_wait_warp(&empty[s], ph)) { ok = false; break; }
+      if (leader) {
+        const uint32_t st = base + s * stage_bytes;
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        tma_load_2d(st, &tmW, &full[s], (kb0 + it) * PK, jt * F_J);
+        tma_load_2d(st + F_J * PK, &tmX, &full[s], (kb0 + it) * PK, tt * p.bn);
+      }
+      if (++s == p.stages) {
+        s = 0;
+        ph ^= 1;
+      }
     }
     for (int j = it - 1; j >= 0 && j >= it - p.stages; --j)  // the last loads have landed
-      if (!mbar_wait(&full[j % p.stages], (j / p.stages) & 1)) ok = false;
-  } else if (warp == 1 && lane == 0) {
-    const uint32_t idesc = idesc_s8_s32(F_J, p.bn);
+      if (!mbar_wait_warp(&full[j % p.stages], (j / p.stages) & 1)) ok = false;
+  } else if (warp == 1) {
+    const bool leader = elect_one();
+    const uint32_t idesc = idesc_s8_s32(F_J, p.bn), dstage = static_cast<uint32_t>(stage_bytes) >> 4;
+    const uint64_t dw0 = smem_desc_sw128(smem_u32(ring), 16, 1024);
+    int s = 0;
+    uint32_t ph = 0;
     for (int it = 0; it < nkb; ++it) {
-      const int s = it % p.stages, r = it / p.stages;
-      if (!mbar_wait(&full[s], r & 1)) { ok = false; break; }
+      if (!mbar_wait_warp(&full[s], ph)) { ok = false; break; }
       tc_fence_after();
-      const uint32_t sw = smem_u32(ring + s * stage_bytes), sx = sw + F_J * PK;
+      if (leader) {
+        const uint64_t dw = dw0 + s * dstage, dx = dw + (F_J * PK >> 4);
+        mma_s8(tmem, dw, dx, idesc, it != 0);
 #pragma unroll
-      for (int kk = 0; kk < PK / 32; ++kk)
-        mma_s8(tmem, smem_desc_sw128(sw + kk * 32, 16, 1024), smem_desc_sw128(sx + kk * 32, 16, 1024),
-               idesc, (it | kk) != 0);
-      mma_commit(&empty[s]);
+        for (int kk = 1; kk < PK / 32; ++kk) mma_s8(tmem, dw + 2 * kk, dx + 2 * kk, idesc, 1u);
+        mma_commit(&empty[s]);
+      }
+      if (++s == p.stages) {
+        s = 0;
+        ph ^= 1;
+      }
     }
-    mma_commit(&acc_full);
+    if (leader) mma_commit(&acc_full);
+  } else if (warp >= 2) {
+    for (int c = threadIdx.x - 64; c < n; c += 64) {
+      xs[c] = a.xs[t0 + c];
+      if (a.wz) xsum[c] = a.xsum[t0 + c];
+      if (c % p.split == rank) {       // M and R of the columns that this CTA finishes: to L2
+        const int64_t j0 = static_cast<int64_t>(jt) * F_J;
+        for (int64_t q = j0; q < j0 + F_J && q < a.d_out; q += 128 / sizeof(T)) {
+          if (a.m) prefetch_l2(static_cast<const T *>(a.m) + (t0 + c) * a.d_out + q);
+          if (a.r) prefetch_l2(static_cast<const T *>(a.r) + (t0 + c) * a.d_out + q);
+        }
+      }
+    }
   }
-  __syncwarp();
+  __syncthreads();
   if (!__all_sync(0xffffffffu, mbar_wait(&acc_full, 0))) ok = false;
   tc_fence_after();
 
-  const int64_t j = static_cast<int64_t>(jt) * F_J + threadIdx.x;
-  const int64_t t0 = static_cast<int64_t>(tt) * p.bn;
-  const int n = a.n_tok - t0 < p.bn ? static_cast<int>(a.n_tok - t0) : p.bn;
   const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-  const bool live = j < a.d_out;
-  const float ws = live ? __half2float(__ushort_as_half(a.ws[j])) : 0.0f;
-  const int wz = live && a.wz ? a.wz[j] : 0;
-  const float bias = live && a.bias ? a.bias[j] : 0.0f;
   if (p.split == 1) {
     for (int c0 = 0; c0 < n; c0 += 32) {
       float v[32];
       tmem_ld32(taddr + c0, v);
-      if (live) {
+      int acc[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c0 + i < n) finish<T>(a, t0 + c0 + i, j, __float_as_int(v[i]), ws, wz, bias);
-      }
+      for (int i = 0; i < 32; ++i) acc[i] = __float_as_int(v[i]);
+      few_columns<T, 32>(a, o, live, t0, c0, 1, n, j, xs, xsum, acc);
     }
     tc_fence_before();
     __syncthreads();
@@ -533,17 +762,19 @@ __global__ void __launch_bounds__(F_THREADS)
     }
     tc_fence_before();
     cluster_sync();
-    if (live) {
-      for (int c = rank; c < n; c += p.split) {
-        const uint32_t at = smem_u32(sums + c * F_J + threadIdx.x);
-        int part[8];
+    for (int c0 = rank; c0 < n; c0 += 16 * p.split) {
+      int acc[16] = {};
+#pragma unroll 2
+      for (int r = 0; r < p.split; ++r) {
+        const uint32_t base = mapa_shared(smem_u32(sums + threadIdx.x), r);
+        int part[16];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) part[r] = r < p.split ? ld_cluster_s32(at, r) : 0;
-        int acc = 0;
+        for (int i = 0; i < 16; ++i)
+          part[i] = c0 + i * p.split < n ? ld_cluster_s32(base + (c0 + i * p.split) * (F_J * 4)) : 0;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) acc += part[r];
-        finish<T>(a, t0 + c, j, acc, ws, wz, bias);
+        for (int i = 0; i < 16; ++i) acc[i] += part[i];
       }
+      few_columns<T, 16>(a, o, live, t0, c0, p.split, n, j, xs, xsum, acc);
     }
     cluster_sync();  // no CTA leaves while another reads its sums
   }
@@ -555,16 +786,93 @@ __global__ void __launch_bounds__(F_THREADS)
   }
 }
 
-// Opts a kernel in to its shared memory, once per device.
-template <typename K>
-void allow_smem(K kernel, size_t bytes, std::atomic<uint64_t> &done) {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  const uint64_t bit = 1ull << (dev & 63);
-  if (done.load(std::memory_order_relaxed) & bit) return;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(bytes)) == cudaSuccess)
-    done.fetch_or(bit, std::memory_order_relaxed);
+// ---------------------------------------------------------------- one to eight tokens
+// A warp reads V_R output rows 512 bytes at a time (16 per lane, two to four
+// steps in flight) straight from global memory and multiplies them with NT tokens by
+// dp4a; `ks` warps of a block share a row group along K and add up through
+// shared memory.  No barriers, no TMEM and no tensor maps to set up: the
+// weights' bytes and one memory round trip are all there is.
+constexpr int V_R = 4, V_WARPS = 4;
+
+__device__ __forceinline__ int4 ld_stream(const int8_t *p) {
+  int4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(V_WARPS * 32) w8a8_vec_kernel(W8Args a, int ks) {
+  __shared__ int part[V_WARPS][V_R * NT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int groups = V_WARPS / ks, kp = warp % ks, grp = warp / ks;
+  const int64_t j0 = (static_cast<int64_t>(blockIdx.x) * groups + grp) * V_R;
+  if (blockIdx.x == 0 && threadIdx.x == 0) reset_status(a.status);
+  int acc[V_R][NT] = {};
+  const int8_t *w[V_R];
+#pragma unroll
+  for (int r = 0; r < V_R; ++r)  // rows past the end read the last one again
+    w[r] = a.w + (j0 + r < a.d_out ? j0 + r : a.d_out - 1) * a.d_in;
+  constexpr int ST = NT == 1 ? 4 : 2;   // steps in flight
+  const int stride = ks * 512;
+  for (int k = kp * 512 + lane * 16; k < a.d_in; k += ST * stride) {
+    int4 wv[ST][V_R], xv[ST][NT];
+#pragma unroll
+    for (int u = 0; u < ST; ++u) {
+      const int ku = k + u * stride;
+      if (ku < a.d_in) {
+#pragma unroll
+        for (int r = 0; r < V_R; ++r) wv[u][r] = ld_stream(w[r] + ku);
+      } else {
+#pragma unroll
+        for (int r = 0; r < V_R; ++r) wv[u][r] = make_int4(0, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < ST; ++u) {
+      const int ku = k + u * stride;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        xv[u][t] = ku < a.d_in
+                       ? __ldg(reinterpret_cast<const int4 *>(a.x + static_cast<int64_t>(t) * a.d_in + ku))
+                       : make_int4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < ST; ++u)
+#pragma unroll
+      for (int r = 0; r < V_R; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          acc[r][t] = __dp4a(wv[u][r].x, xv[u][t].x, acc[r][t]);
+          acc[r][t] = __dp4a(wv[u][r].y, xv[u][t].y, acc[r][t]);
+          acc[r][t] = __dp4a(wv[u][r].z, xv[u][t].z, acc[r][t]);
+          acc[r][t] = __dp4a(wv[u][r].w, xv[u][t].w, acc[r][t]);
+        }
+  }
+#pragma unroll
+  for (int r = 0; r < V_R; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int v = __reduce_add_sync(0xffffffffu, acc[r][t]);
+      if (lane == 0) part[warp][r * NT + t] = v;
+    }
+  __syncthreads();
+  // thread (group, token, row): one output
+  const int i = threadIdx.x;
+  if (i < groups * V_R * NT) {
+    const int r = i % V_R, g = i / V_R % groups, t = i / (V_R * groups);
+    const int64_t j = (static_cast<int64_t>(blockIdx.x) * groups + g) * V_R + r;
+    if (j < a.d_out) {
+      int sum = 0;
+      for (int q = 0; q < ks; ++q) sum += part[g * ks + q][r * NT + t];
+      const int64_t at = t * a.d_out + j;
+      from_f(finish(a, out_col(a, j, true), sum, a.xs[t], a.wz ? a.xsum[t] : 0,
+                    a.m ? to_f(static_cast<const T *>(a.m)[at]) : 0.0f,
+                    a.r ? to_f(static_cast<const T *>(a.r)[at]) : 0.0f),
+             static_cast<T *>(a.y)[at]);
+    }
+  }
 }
 
 template <typename T>
@@ -572,32 +880,35 @@ constexpr CUtensorMapDataType tmap_type() {
   return sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 }
 
-template <typename T>
+template <typename T, int PJ>
 gq_status launch_pair(W8Args a, cudaStream_t st) {
-  static std::atomic<uint64_t> done{0};
+  using S = PairShape<PJ>;
+  static SmemOptIn opt;
   CUtensorMap tX, tW, tY{};
   gq_status s = make_tmap_2d(&tX, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.d_in, a.n_tok, a.d_in, PK, 128);
   if (s == GQ_OK)
-    s = make_tmap_2d(&tW, a.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.d_in, a.d_out, a.d_in, PK, 128);
+    s = make_tmap_2d(&tW, a.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.d_in, a.d_out, a.d_in, PK, PJ / 2);
   if (s == GQ_OK && a.y_vec)
-    s = make_tmap_2d(&tY, a.y, tmap_type<T>(), sizeof(T), a.d_out, a.n_tok, a.d_out, 128 / sizeof(T), 32);
+    s = make_tmap_2d(&tY, a.y, tmap_type<T>(), sizeof(T), a.d_out, a.n_tok, a.d_out, 64 / sizeof(T),
+                     32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (s != GQ_OK) return s;
   a.y_tma = a.y_vec;
   a.n_tt = static_cast<int>((a.n_tok + PT - 1) / PT);
   a.n_jt = static_cast<int>((a.d_out + PJ - 1) / PJ);
   a.nkb = (a.d_in + PK - 1) / PK;
   const int tiles = a.n_tt * a.n_jt, pairs = num_sms() / 2;
-  allow_smem(w8a8_pair_kernel<T>, P_SMEM, done);
+  opt.allow(w8a8_pair_kernel<T, PJ>, S::kSmem);
   const int slot = timer_begin(GQ_KERNEL_W8A8, st);
-  w8a8_pair_kernel<T><<<2 * (tiles < pairs ? tiles : pairs), P_THREADS, P_SMEM, st>>>(tX, tW, tY, a);
+  w8a8_pair_kernel<T, PJ><<<2 * (tiles < pairs ? tiles : pairs), S::kThreads, S::kSmem, st>>>(tX, tW, tY, a);
   count_launch();
   timer_end(slot, st, 2.0 * static_cast<double>(a.n_tok) * a.d_out * a.d_in);
   return check_launch("w8a8_pair_kernel");
 }
 
-// Clusters of CTAs per tile: enough of them for two CTAs per SM, each with
-// at least four K steps.  A CTA of a split tile so holds four stages or its
-// share of 108 KB, 72 KB and more: it never shares an SM with a CTA of a
+// CTAs per tile: the split whose fullest SM has the fewest K steps, the
+// smallest such; each CTA keeps at least four steps.  The SM's shared memory
+// is divided among the CTAs that it then holds (at most three).  A CTA of a
+// split tile holds 72 KB or more: it never shares an SM with a CTA of a
 // kernel that takes all of TMEM (their shared memory is above 190 KB), and
 // at most three of them, 384 columns, share one, so no cluster waits for
 // TMEM columns while it holds some that another cluster waits for.
@@ -608,31 +919,44 @@ FewPlan few_plan(int64_t n_tok, int64_t d_out, int nkb, int &n_tt, int &n_jt) {
   p.bn = static_cast<int>((per + 15) / 16 * 16);
   n_jt = static_cast<int>((d_out + F_J - 1) / F_J);
   const int64_t tiles = static_cast<int64_t>(n_tt) * n_jt;
+  const int sms = num_sms();
+  int64_t best = INT64_MAX, per_sm = 1;
   p.split = 1;
-  while (p.split < 8 && tiles * p.split * 2 <= 2 * num_sms() + num_sms() / 2 && nkb >= 8 * p.split) p.split *= 2;
+  for (int c = 1; c <= 8 && (c == 1 || nkb >= 4 * c); ++c) {
+    const int64_t held = (tiles * c + sms - 1) / sms;
+    if (c > 1 && held > 2) break;
+    const int64_t cost = held * ((nkb + c - 1) / c);
+    if (cost < best) {
+      best = cost;
+      p.split = c;
+      per_sm = held;
+    }
+  }
+  p.steps = static_cast<int>(best < INT32_MAX ? best : INT32_MAX);
   const int stage = (F_J + p.bn) * PK;
-  p.stages = (108 * 1024) / stage;
+  const int kb = per_sm == 1 ? 216 : per_sm == 2 ? 108 : 72;
+  p.stages = kb * 1024 / stage;
   if (p.stages > F_MAX_STAGES) p.stages = F_MAX_STAGES;
   const int most = (nkb + p.split - 1) / p.split;
-  const int need = p.split > 1 ? (p.bn * F_J * 4 + stage - 1) / stage : 1;
-  if (p.stages > most) p.stages = most > need ? most : need;
+  // a split tile's sums lie in the ring, which is at least 72 KB then
+  const int need = p.split > 1 ? ((p.bn > 128 ? p.bn * 512 : 72 * 1024) + stage - 1) / stage : 1;
+  if (p.stages > most) p.stages = most;
+  if (p.stages < need) p.stages = need;
   p.tmem_cols = 32;
   while (p.tmem_cols < p.bn) p.tmem_cols *= 2;
   return p;
 }
 
 template <typename T>
-gq_status launch_few(W8Args a, cudaStream_t st) {
-  static std::atomic<uint64_t> done{0};
-  a.nkb = (a.d_in + PK - 1) / PK;
-  const FewPlan p = few_plan(a.n_tok, a.d_out, a.nkb, a.n_tt, a.n_jt);
+gq_status launch_few(const W8Args &a, const FewPlan &p, cudaStream_t st) {
+  static SmemOptIn opt;
   CUtensorMap tX, tW;
   gq_status s = make_tmap_2d(&tX, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.d_in, a.n_tok, a.d_in, PK, p.bn);
   if (s == GQ_OK)
     s = make_tmap_2d(&tW, a.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.d_in, a.d_out, a.d_in, PK, F_J);
   if (s != GQ_OK) return s;
   const size_t smem = 1024 + static_cast<size_t>(p.stages) * (F_J + p.bn) * PK;
-  allow_smem(w8a8_few_kernel<T>, 1024 + 108 * 1024, done);
+  opt.allow(w8a8_few_kernel<T>, 1024 + 216 * 1024);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(a.n_tt) * a.n_jt * p.split);
   cfg.blockDim = dim3(F_THREADS);
@@ -651,11 +975,72 @@ gq_status launch_few(W8Args a, cudaStream_t st) {
   return check_launch("w8a8_few_kernel");
 }
 
+template <typename T, int NT>
+gq_status launch_vec_n(const W8Args &a, cudaStream_t st) {
+  // warps along K: while the row groups alone do not fill the SMs
+  int ks = 1;
+  const int64_t rows = (a.d_out + V_R - 1) / V_R;
+  while (ks < V_WARPS && rows * ks < 8 * static_cast<int64_t>(num_sms()) && a.d_in > 512 * ks) ks *= 2;
+  const int64_t groups = V_WARPS / ks;
+  const int slot = timer_begin(GQ_KERNEL_W8A8, st);
+  w8a8_vec_kernel<T, NT><<<static_cast<unsigned>((rows + groups - 1) / groups), V_WARPS * 32, 0, st>>>(a, ks);
+  count_launch();
+  timer_end(slot, st, 2.0 * static_cast<double>(a.n_tok) * a.d_out * a.d_in);
+  return check_launch("w8a8_vec_kernel");
+}
+
+template <typename T>
+gq_status launch_vec(const W8Args &a, cudaStream_t st) {
+  switch (a.n_tok) {
+    case 1: return launch_vec_n<T, 1>(a, st);
+    case 2: return launch_vec_n<T, 2>(a, st);
+    case 3: return launch_vec_n<T, 3>(a, st);
+    case 4: return launch_vec_n<T, 4>(a, st);
+    case 5: return launch_vec_n<T, 5>(a, st);
+    case 6: return launch_vec_n<T, 6>(a, st);
+    case 7: return launch_vec_n<T, 7>(a, st);
+    default: return launch_vec_n<T, 8>(a, st);
+  }
+}
+
+// Expected microseconds of a pair kernel: launch and first loads, a round of
+// tiles per 74 pairs, each bound by its MMAs or by its epilogue (rows of Y
+// that TMA cannot store, fp32), and the last epilogue.  Steps of 0.35 (PJ =
+// 256) and 0.25 us (128) as measured: an N = 128 MMA reads its A tile twice
+// as often per flop.
+template <typename T, int PJ>
+float pair_us(const W8Args &a, int nkb) {
+  const int64_t tiles = ((a.n_tok + PT - 1) / PT) * ((a.d_out + PJ - 1) / PJ), pairs = num_sms() / 2;
+  const float rounds = static_cast<float>((tiles + pairs - 1) / pairs);
+  const float epi = (PJ == 256 ? 3.0f : 2.0f) * (sizeof(T) == 4 ? 1.7f : 1.0f) * (a.y_vec ? 1.0f : 1.7f);
+  const float mma = static_cast<float>(nkb) * (PJ == 256 ? 0.35f : 0.25f);
+  return 5.5f + rounds * (mma > epi ? mma : epi) + epi;
+}
+
+// The kernel is chosen by these estimates.  Measured (us, graph replays, bf16
+// out, one per call below the line taken):
+//   n   d_in  d_out    vec   few   256   128
+//   4   2048   8192    6.4   8.7     -     -
+//   8   2048   8192    9.7   8.8     -     -
+//   33  8192   8192      -  19.2  27.3  20.6
+//   48  4096  11008      -  15.3  18.9  19.0
+//   256 8192   8192      -  25.3  28.4  21.9
+//   512 8192   8192      -  35.2  29.2  31.5
+//  2048 4096  11008      -     -  62.6  69.1
 template <typename T>
 gq_status launch_typed(W8Args a, cudaStream_t st) {
   a.y_vec = a.d_out * sizeof(T) % 16 == 0;
-  if (a.n_tok > 256) return launch_pair<T>(a, st);
-  return launch_few<T>(a, st);
+  if (a.n_tok <= 3 || (a.n_tok <= 8 && a.n_tok * a.d_in * a.d_out < (int64_t(1) << 27)))
+    return launch_vec<T>(a, st);
+  W8Args f = a;
+  f.nkb = (a.d_in + PK - 1) / PK;
+  const FewPlan p = few_plan(a.n_tok, a.d_out, f.nkb, f.n_tt, f.n_jt);
+  // a CTA's loads arrive at about 50 GB/s; an unsplit SM's epilogues overlap
+  const float few = 5.0f + static_cast<float>(p.steps) * static_cast<float>((F_J + p.bn) * PK) / 50e3f +
+                    (p.split > 1 ? 1.5f : 0.0f) + 0.035f * static_cast<float>(p.bn);
+  const float wide = pair_us<T, 256>(a, f.nkb), narrow = pair_us<T, 128>(a, f.nkb);
+  if (few <= wide && few <= narrow) return launch_few<T>(f, p, st);
+  return wide <= narrow ? launch_pair<T, 256>(a, st) : launch_pair<T, 128>(a, st);
 }
 
 }  // namespace
