@@ -25,6 +25,12 @@ gq_status check_launch(const char *what) {
   return fail(GQ_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
+gq_status launched(cudaError_t e, const char *what) {
+  if (e == cudaSuccess) return check_launch(what);
+  cudaGetLastError();
+  return fail(GQ_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
 int num_sms() {
   static int cache[64] = {0};
   int dev = 0;

@@ -141,6 +141,17 @@ __device__ __forceinline__ bool mbar_wait_cluster_warp(uint64_t *bar, uint32_t p
   return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity));
 }
 
+// Chained launches (launch_chained): chain_wait returns when the stream's
+// earlier work has completed and its memory is visible; every thread of such
+// a kernel calls it before its first access to global memory, so that a
+// kernel has completed only after everything before it.  chain_next lets the
+// next chained launch's blocks start and set themselves up; a kernel calls
+// it when its blocks hold the tensor memory that they need.
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void chain_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");

@@ -37,6 +37,8 @@ void clear_error();
 gq_status fail(gq_status s, const std::string &msg);
 // GQ_ERR_CUDA with the text of the pending CUDA error, or GQ_OK.
 gq_status check_launch(const char *what);
+// The same for a launch that returned its error.
+gq_status launched(cudaError_t e, const char *what);
 
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -49,6 +51,29 @@ gq_status make_tmap_2d(CUtensorMap *map, const void *base, CUtensorMapDataType d
                        CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 int num_sms();
+
+// Launches a kernel that waits for the stream's earlier work by itself
+// (chain_wait), so that its launch and its blocks' set-up run beside the end
+// of the kernel before it (a decode step's products 12.1 -> 10.2 us each from
+// a stream at 4096 -> 11008); `cluster` CTAs per cluster.
+template <typename... KA, typename... A>
+cudaError_t launch_chained(void (*kernel)(KA...), unsigned grid, unsigned block, size_t smem,
+                           cudaStream_t st, int cluster, const A &...args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, KA(args)...);
+}
 
 // Opts one kernel in to its dynamic shared memory, once per device (a static
 // of the function that launches it).

@@ -365,6 +365,8 @@ __global__ void __launch_bounds__(N == 8 ? 1024 : 256, N == 8 ? 1 : 3) quant_blo
   constexpr bool NORM = MODE == kNorm;
   constexpr int E = kE<T>, U = N / E;
   __shared__ uint64_t slots[2][32], mine[2];
+  chain_wait();
+  chain_next();
   const int part = threadIdx.x / a.team, tid = threadIdx.x - part * a.team;
   const int rank = a.split > 1 ? static_cast<int>(blockIdx.x) % a.split : 0;
   const int64_t row = static_cast<int64_t>(blockIdx.x / a.split) * a.rows + part;
@@ -459,13 +461,19 @@ __device__ __forceinline__ void sts16(uint32_t p, const uint4 &v) {
                "r"(v.w) : "memory");
 }
 
-template <typename T, typename WT, Mode MODE, int AHEAD, bool WREG>
+// FULL: every thread has all its units (d_in = 32 team), so that no unit is a
+// branch of its own.  For 16-bit rows with column factors, which are bound by
+// the instructions issued: 16384 x 28672 278 -> 263 us (plain rows, bound by
+// HBM, 220 -> 250: not there).
+template <typename T, typename WT, Mode MODE, int AHEAD, bool WREG, bool FULL>
 __global__ void __launch_bounds__(WREG ? kRegThreads : 1024, 1) quant_rows_kernel(const QuantArgs a) {
   constexpr bool NORM = MODE == kNorm;
   constexpr int E = kE<T>, U = 32 / E;
   extern __shared__ uint4 ring[];
   __shared__ uint64_t slots[2][32];
   __shared__ int sums[2][32];
+  chain_wait();
+  chain_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int part = threadIdx.x / a.team, tid = threadIdx.x - part * a.team;
   const int tw = a.team >> 5, w0 = warp / tw * tw;
@@ -474,7 +482,8 @@ __global__ void __launch_bounds__(WREG ? kRegThreads : 1024, 1) quant_rows_kerne
   const uint32_t piece = blockDim.x * 16, rowb = piece * U * (res ? 2 : 1);
   const uint32_t sbase = smem_u32(ring) + threadIdx.x * 16;
   const int c0 = tid * E, cs = a.team * E;
-  const int nv = c0 < a.d_in ? (a.d_in - c0 + cs - 1) / cs : 0;   // this thread's units of a row
+  // this thread's units of a row
+  const int nv = FULL ? U : c0 < a.d_in ? (a.d_in - c0 + cs - 1) / cs : 0;
   const int64_t step = static_cast<int64_t>(gridDim.x) * a.rows;
   int64_t row = static_cast<int64_t>(blockIdx.x) * a.rows + part;
   const char *xn = reinterpret_cast<const char *>(static_cast<const T *>(a.x) + row * a.ldx + c0);
@@ -486,7 +495,7 @@ __global__ void __launch_bounds__(WREG ? kRegThreads : 1024, 1) quant_rows_kerne
     if (ahead < a.n_tok) {
 #pragma unroll
       for (int v = 0; v < U; ++v)
-        if (v < nv) {
+        if (FULL || v < nv) {
           cp_async16(at + v * piece, xn + v * unitb);
           if (res) cp_async16(at + (U + v) * piece, rn + v * unitb);
         }
@@ -533,25 +542,38 @@ __global__ void __launch_bounds__(WREG ? kRegThreads : 1024, 1) quant_rows_kerne
   int64_t last = -1;
   // (all teams of a block make the same number of rounds)
   for (; row - part < a.n_tok; row += step, par ^= 1) {
-    const int n = row < a.n_tok ? nv : 0;
+    const bool live = row < a.n_tok;
+    const int n = live ? nv : 0;
     uint4 x[U];
     Stats<MODE, T> st;
     asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+    if constexpr (NORM) {
 #pragma unroll
-    for (int v = 0; v < U; ++v)
-      if (v < n) {
-        x[v] = lds16(slot + v * piece);
-        if (res) {
-          x[v] = add_residual<T>(x[v], lds16(slot + (U + v) * piece));
-          *reinterpret_cast<uint4 *>(static_cast<T *>(a.h) + at + v * cs) = x[v];
+      for (int v = 0; v < U; ++v)
+        if (v < n) {
+          x[v] = lds16(slot + v * piece);
+          if (res) {
+            x[v] = add_residual<T>(x[v], lds16(slot + (U + v) * piece));
+            *reinterpret_cast<uint4 *>(static_cast<T *>(a.h) + at + v * cs) = x[v];
+          }
         }
-      }
 #pragma unroll
-    for (int v = 0; v < U; ++v)
-      if (v < n) {
-        uint64_t g[E / 2];
-        st.take(x[v], factors(v), g);
-      }
+      for (int v = 0; v < U; ++v)
+        if (v < n) {
+          uint64_t g[E / 2];
+          st.take(x[v], factors(v), g);
+        }
+    } else if (live) {
+#pragma unroll
+      for (int v = 0; v < U; ++v)
+        if (FULL || v < n) x[v] = lds16(slot + v * piece);
+#pragma unroll
+      for (int v = 0; v < U; ++v)
+        if (FULL || v < n) {
+          uint64_t g[E / 2];
+          st.take(x[v], factors(v), g);
+        }
+    }
     issue(slot);                               // the row of this slot is in registers
     slot = AHEAD == 2 && slot == sbase ? sbase + rowb : sbase;
     uint32_t bits = st.bits();
@@ -576,24 +598,27 @@ __global__ void __launch_bounds__(WREG ? kRegThreads : 1024, 1) quant_rows_kerne
     }
     const RowGrid gr = row_grid(bits);
     int sum = 0;
+    if (live) {
+      int8_t *out = a.codes + at;
 #pragma unroll
-    for (int v = 0; v < U; ++v)
-      if (v < n) {
-        uint64_t g[E / 2];
-        widen(x[v], g, T());
-        if (MODE != kPlain) factors(v).times(g);
-        sum += put(g, gr, a.codes + at + v * cs);
-      }
+      for (int v = 0; v < U; ++v)
+        if (FULL || v < n) {
+          uint64_t g[E / 2];
+          widen(x[v], g, T());
+          if (MODE != kPlain) factors(v).times(g);
+          sum += put(g, gr, out + v * cs);
+        }
+    }
     if (a.sums) {
       sum = __reduce_add_sync(0xffffffffu, sum);
       if (lane == 0) sums[par][warp] = sum;
     }
-    if (warp == w0 && row < a.n_tok) {
+    if (warp == w0 && live) {
       const float s = row_scale<T, NORM>(a, gr, ssq, res ? static_cast<const T *>(a.h) + row * a.d_in
                                                          : static_cast<const T *>(a.x) + row * a.ldx);
       if (lane == 0) a.scales[row] = s;
     }
-    last = row < a.n_tok ? row : -1;
+    last = live ? row : -1;
     at += step * a.d_in;
   }
   if (a.sums) {
@@ -610,35 +635,26 @@ __global__ void __launch_bounds__(WREG ? kRegThreads : 1024, 1) quant_rows_kerne
 template <typename T, Mode MODE>
 constexpr int kAhead = sizeof(T) == 2 && MODE == kPlain ? 2 : 1;
 
-template <typename T, typename WT, Mode MODE, bool WREG>
+template <typename T, typename WT, Mode MODE, bool WREG, bool FULL>
 cudaError_t launch_many(const QuantArgs &a, size_t smem, cudaStream_t st) {
   static SmemOptIn opt;
-  opt.allow(quant_rows_kernel<T, WT, MODE, kAhead<T, MODE>, WREG>, kRingMost);
+  const auto kernel = quant_rows_kernel<T, WT, MODE, kAhead<T, MODE>, WREG, FULL>;
+  opt.allow(kernel, kRingMost);
   const int threads = a.rows * a.team;
   int per_sm = (WREG ? kRegThreads : 1024) / threads;
   if (per_sm > static_cast<int>(kRingMost / (smem + 2048))) per_sm = static_cast<int>(kRingMost / (smem + 2048));
   if (per_sm < 1) per_sm = 1;
   const int64_t blocks = (a.n_tok + a.rows - 1) / a.rows, most = static_cast<int64_t>(num_sms()) * per_sm;
-  quant_rows_kernel<T, WT, MODE, kAhead<T, MODE>, WREG>
-      <<<static_cast<unsigned>(blocks < most ? blocks : most), threads, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_chained(kernel, static_cast<unsigned>(blocks < most ? blocks : most), threads, smem, st, 1, a);
 }
 
 template <typename T, typename WT, Mode MODE, int N>
 cudaError_t launch_block(QuantArgs a, cudaStream_t st) {
   a.team = ((a.per + N - 1) / N + 31) / 32 * 32;
   a.rows = N == 8 || a.split > 1 || a.team > 128 ? 1 : 256 / a.team;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.n_tok + a.rows - 1) / a.rows * a.split));
-  cfg.blockDim = dim3(a.rows * a.team);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = a.split;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = a.split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, quant_block_kernel<T, WT, MODE, N>, a);
+  return launch_chained(quant_block_kernel<T, WT, MODE, N>,
+                        static_cast<unsigned>((a.n_tok + a.rows - 1) / a.rows * a.split), a.rows * a.team, 0,
+                        st, a.split, a);
 }
 
 template <typename T, typename WT, Mode MODE>
@@ -649,6 +665,7 @@ gq_status launch_rows(QuantArgs a, cudaStream_t st) {
   m.team = ((a.d_in + 31) / 32 + 31) / 32 * 32;
   m.rows = m.team >= 128 ? 1 : 128 / m.team;
   constexpr bool kCanReg = sizeof(T) == 4 && MODE != kPlain;
+  constexpr bool kFull = sizeof(T) == 2 && MODE == kCol;
   const bool wreg = kCanReg && m.team <= kRegThreads;
   const size_t smem = static_cast<size_t>(m.rows * m.team) *
                       (32 * sizeof(T) * kAhead<T, MODE> * (a.r ? 2 : 1) + (MODE == kPlain || wreg ? 0 : 128));
@@ -665,17 +682,18 @@ gq_status launch_rows(QuantArgs a, cudaStream_t st) {
   else if (elems <= sms * 768 * 32 || m.team > 1024 || smem > kRingMost)
     e = launch_block<T, WT, MODE, 32>(a, st);
   else if (wreg)
-    e = launch_many<T, WT, MODE, kCanReg>(m, smem, st);
+    e = launch_many<T, WT, MODE, kCanReg, false>(m, smem, st);
+  else if (kFull && a.d_in == 32 * m.team)
+    e = launch_many<T, WT, MODE, false, kFull>(m, smem, st);
   else
-    e = launch_many<T, WT, MODE, false>(m, smem, st);
+    e = launch_many<T, WT, MODE, false, false>(m, smem, st);
   count_launch();
   timer_end(slot, st,
             static_cast<double>(a.n_tok) *
                     (static_cast<double>(a.d_in) * (sizeof(T) * (a.r ? 3 : 1) + 1) + 4 +
                      (a.sums ? 4 : 0)) +
                 (a.w ? static_cast<double>(a.d_in) * sizeof(WT) : 0.0));
-  return e == cudaSuccess ? check_launch("quant_rows_kernel")
-                          : fail(GQ_ERR_CUDA, std::string("quant kernel: ") + cudaGetErrorString(e));
+  return launched(e, "quant kernel");
 }
 
 // 16 codes per thread from the packed bit stream.

@@ -310,7 +310,7 @@ __device__ __forceinline__ void pair_tile(int t, int n_tt, int n_jt, int &tt, in
 }
 
 template <typename T, int PJ>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<PJ>::kThreads, 1)
+__global__ void __launch_bounds__(PairShape<PJ>::kThreads, 1)
     w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX,
                      const __grid_constant__ CUtensorMap tmW,
                      const __grid_constant__ CUtensorMap tmY, W8Args a) {
@@ -333,7 +333,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<PJ>::kThre
   const int pair = static_cast<int>(blockIdx.x >> 1), n_pairs = static_cast<int>(gridDim.x >> 1);
   const int n_tiles = a.n_tt * a.n_jt;
   if (threadIdx.x == 0) {
-    if (blockIdx.x == 0) reset_status(a.status);
     for (int s = 0; s < P_STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -347,6 +346,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<PJ>::kThre
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
   }
+  chain_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) reset_status(a.status);
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 2 * PJ);
     tmem_relinquish_pair();
@@ -355,6 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<PJ>::kThre
   cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  chain_next();
   const int half0 = static_cast<int>(rank) * 128;  // this CTA's token rows in a tile
 
   if (warp == 0) {
@@ -652,7 +654,6 @@ __global__ void __launch_bounds__(F_THREADS)
   const int kb0 = static_cast<int>(static_cast<int64_t>(a.nkb) * rank / p.split);
   const int nkb = static_cast<int>(static_cast<int64_t>(a.nkb) * (rank + 1) / p.split) - kb0;
   if (threadIdx.x == 0) {
-    if (blockIdx.x == 0) reset_status(a.status);
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -662,6 +663,8 @@ __global__ void __launch_bounds__(F_THREADS)
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
   }
+  chain_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) reset_status(a.status);
   if (warp == 1) {
     tmem_alloc(&tmem_slot, static_cast<uint32_t>(p.tmem_cols));
     tmem_relinquish();
@@ -676,6 +679,7 @@ __global__ void __launch_bounds__(F_THREADS)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  chain_next();
 
   bool ok = true;
   if (warp == 0) {
@@ -808,6 +812,8 @@ __global__ void __launch_bounds__(V_WARPS * 32) w8a8_vec_kernel(W8Args a, int ks
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = V_WARPS / ks, kp = warp % ks, grp = warp / ks;
   const int64_t j0 = (static_cast<int64_t>(blockIdx.x) * groups + grp) * V_R;
+  chain_wait();
+  chain_next();
   if (blockIdx.x == 0 && threadIdx.x == 0) reset_status(a.status);
   int acc[V_R][NT] = {};
   const int8_t *w[V_R];
@@ -899,10 +905,11 @@ gq_status launch_pair(W8Args a, cudaStream_t st) {
   const int tiles = a.n_tt * a.n_jt, pairs = num_sms() / 2;
   opt.allow(w8a8_pair_kernel<T, PJ>, S::kSmem);
   const int slot = timer_begin(GQ_KERNEL_W8A8, st);
-  w8a8_pair_kernel<T, PJ><<<2 * (tiles < pairs ? tiles : pairs), S::kThreads, S::kSmem, st>>>(tX, tW, tY, a);
+  const cudaError_t e = launch_chained(w8a8_pair_kernel<T, PJ>, 2 * (tiles < pairs ? tiles : pairs),
+                                       S::kThreads, S::kSmem, st, 2, tX, tW, tY, a);
   count_launch();
   timer_end(slot, st, 2.0 * static_cast<double>(a.n_tok) * a.d_out * a.d_in);
-  return check_launch("w8a8_pair_kernel");
+  return launched(e, "w8a8_pair_kernel");
 }
 
 // CTAs per tile: the split whose fullest SM has the fewest K steps, the
@@ -957,22 +964,12 @@ gq_status launch_few(const W8Args &a, const FewPlan &p, cudaStream_t st) {
   if (s != GQ_OK) return s;
   const size_t smem = 1024 + static_cast<size_t>(p.stages) * (F_J + p.bn) * PK;
   opt.allow(w8a8_few_kernel<T>, 1024 + 216 * 1024);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.n_tt) * a.n_jt * p.split);
-  cfg.blockDim = dim3(F_THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = p.split;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = p.split > 1 ? 1 : 0;
   const int slot = timer_begin(GQ_KERNEL_W8A8, st);
-  cudaLaunchKernelEx(&cfg, w8a8_few_kernel<T>, tX, tW, a, p);
+  const cudaError_t e = launch_chained(w8a8_few_kernel<T>, static_cast<unsigned>(a.n_tt) * a.n_jt * p.split,
+                                       F_THREADS, smem, st, p.split, tX, tW, a, p);
   count_launch();
   timer_end(slot, st, 2.0 * static_cast<double>(a.n_tok) * a.d_out * a.d_in);
-  return check_launch("w8a8_few_kernel");
+  return launched(e, "w8a8_few_kernel");
 }
 
 template <typename T, int NT>
@@ -983,10 +980,11 @@ gq_status launch_vec_n(const W8Args &a, cudaStream_t st) {
   while (ks < V_WARPS && rows * ks < 8 * static_cast<int64_t>(num_sms()) && a.d_in > 512 * ks) ks *= 2;
   const int64_t groups = V_WARPS / ks;
   const int slot = timer_begin(GQ_KERNEL_W8A8, st);
-  w8a8_vec_kernel<T, NT><<<static_cast<unsigned>((rows + groups - 1) / groups), V_WARPS * 32, 0, st>>>(a, ks);
+  const cudaError_t e = launch_chained(w8a8_vec_kernel<T, NT>, static_cast<unsigned>((rows + groups - 1) / groups),
+                                       V_WARPS * 32, 0, st, 1, a, ks);
   count_launch();
   timer_end(slot, st, 2.0 * static_cast<double>(a.n_tok) * a.d_out * a.d_in);
-  return check_launch("w8a8_vec_kernel");
+  return launched(e, "w8a8_vec_kernel");
 }
 
 template <typename T>

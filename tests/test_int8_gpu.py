@@ -501,6 +501,41 @@ def test_two_streams_share_a_workspace():
     assert gq.workspace_status(ws) == 0
 
 
+@pytest.mark.parametrize("n", [1, 6, 40, 300])
+def test_calls_behind_one_another_see_each_others_results(n):
+    """Launches overlap (a call's blocks start before the call before it is done): a long chain of
+    dependent calls, with torch's own kernels writing inputs and overwriting outputs between them,
+    gives what the same chain gives with a synchronisation behind every call."""
+    d = 512
+    w, _, _ = _mlp_layers(d, d)
+    nw = torch.linspace(0.5, 1.5, d, device="cuda")
+
+    def chain(sync):
+        x, h = _x(n, d, "bf16").cuda(), _x(n, d, "bf16", seed=1).cuda()
+        tok = dict(codes=torch.empty(n, d, dtype=torch.int8, device="cuda"),
+                   scales=torch.empty(n, device="cuda"), sums=None)
+        y, outs = torch.empty_like(x), []
+        for i in range(40):
+            q = gq.rmsnorm_quantize_int8(x, nw, R=h, H=h, out=tok)
+            sync()
+            gq.w8a8_matmul(w, q, act="silu", Y=y)
+            sync()
+            gq.quantize_tokens_int8(y, out=tok)
+            sync()
+            gq.w8a8_matmul(w, tok, R=y, Y=x)
+            sync()
+            if i % 8 == 3:
+                outs.append(x + 0)
+                x.mul_(0.25)
+                y.fill_(float("nan"))
+                h.mul_(0.5)
+        return outs + [x, h]
+    ref = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        got = chain(lambda: None)
+        assert all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
 def test_results_do_not_change_from_run_to_run():
     w1, _, w3 = _mlp_layers(1024, 1536)
     for n in (1, 24, 200, 600):
