@@ -164,6 +164,9 @@ __device__ __forceinline__ void scale32(const W8Args &a, const float *s, const i
 __device__ __forceinline__ void prefetch_l2(const void *p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
+__device__ __forceinline__ void prefetch_l2(const void *p, int bytes) {  // multiples of 16
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 // M or R over a box of 32 tokens x BC = 64 / sizeof(T) outputs: four lanes
 // take a row's 64 bytes (a lane per row would touch 32 lines an instruction:
 // 2560 x 2048 x 8192 with a residual 51 against 40 us), and the rows change
@@ -267,35 +270,46 @@ __device__ __forceinline__ void store_box(const W8Args &a, const uint8_t *stg, i
 //               of two PJ-column TMEM accumulators; each CTA receives its 128
 //               tokens' rows
 //   the others  epilogue, a warp per 32 tokens x 64 outputs, a thread per
-//               token: the columns' scales, zero-points and bias come once
-//               per tile through shared memory, loaded a tile ahead; results
+//               token: the outputs' scales, zero-points and bias pass through
+//               shared memory of the warp's own, loaded a tile ahead; results
 //               pass a 64-byte-swizzled buffer of the warp's own and leave
 //               by TMA store (by coalesced stores where Y's rows are no
-//               multiple of 16 bytes).
+//               multiple of 16 bytes).  No warp waits for another one's tile
+//               (operands shared by a barrier of all: 2560 x 2048 x 8192 with
+//               GELU 42.7 us, so 40.5).
+// The issuing warps' lanes walk their loops together, so that a step's values
+// stay in uniform registers (a loop of one lane: 0.35 us a step, so 0.25: they
+// share their schedulers with the epilogue).  Bound by the tensor cores where K
+// is long (8192 x 8192 x 28672: 1140 us = 3370 TOP/s in bursts), by the
+// epilogue, about 4 us a tile of 256 x 256, where it is short, up to 2048 or so.
+// Shared memory goes to operand stages first: 4 of them with two staged boxes
+// per warp take 44 us instead of 35 at 2560 x 2048 x 8192, so deep is the
+// loads' latency.
 constexpr int PT = 256, PK = 128;
 constexpr int P_STAGING = 2048;                        // per epilogue warp: 32 rows x 64 bytes
 
+struct Cols {              // operands of an epilogue warp's outputs, in shared memory
+  float s[64];
+  int z[64];
+  float b[64];
+};
 template <int PJ>
 struct PairShape {
   static constexpr int kStages = PJ == 256 ? 5 : 7;
+  static constexpr int kBoxes = PJ == 256 ? 1 : 2;       // staged boxes per epilogue warp
   static constexpr int kX = 128 * PK, kW = PJ / 2 * PK;  // one CTA's operands of a stage
   static constexpr int kStage = kX + kW;
   static constexpr int kWarps = PJ / 16;                 // of the epilogue
   static constexpr int kCols = 64;                       // outputs of each of its warps
   static constexpr int kThreads = 64 + 32 * kWarps;
-  static constexpr size_t kSmem = 1024 + kStages * kStage + kWarps * P_STAGING + 2 * PJ * 12 + 256;
+  static constexpr int kStaging = kBoxes * P_STAGING;
+  static constexpr size_t kSmem = 1024 + kStages * kStage + kWarps * (kStaging + sizeof(Cols)) + 256;
 };
-
-template <int PJ>
-struct Cols {              // per-output operands of a tile, in shared memory
-  float s[PJ];
-  int z[PJ];
-  float b[PJ];
-};
-struct TileOps {           // what one thread brings for a tile: a column's and its token's
-  uint16_t ws;
-  int wz;
-  float bias, xs;
+struct TileOps {           // what one thread brings for a tile: two outputs' operands, its token's
+  int tt, jt;              // the tile
+  uint16_t ws[2];
+  int wz[2];
+  float bias[2], xs;
   int xsum;
 };
 
@@ -315,15 +329,14 @@ __global__ void __launch_bounds__(PairShape<PJ>::kThreads, 1)
                      const __grid_constant__ CUtensorMap tmW,
                      const __grid_constant__ CUtensorMap tmY, W8Args a) {
   using S = PairShape<PJ>;
-  constexpr int P_STAGES = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t *staging = smem + P_STAGES * S::kStage;
-  Cols<PJ> *cols = reinterpret_cast<Cols<PJ> *>(staging + S::kWarps * P_STAGING);
-  uint64_t *full = reinterpret_cast<uint64_t *>(cols + 2);  // CTA 0: both CTAs' loads landed
-  uint64_t *empty = full + P_STAGES;                        // per CTA: MMAs done with the stage
-  uint64_t *acc_full = empty + P_STAGES;                    // per CTA
+  uint8_t *staging = smem + S::kStages * S::kStage;
+  Cols *cols = reinterpret_cast<Cols *>(staging + S::kWarps * S::kStaging);
+  uint64_t *full = reinterpret_cast<uint64_t *>(cols + S::kWarps);  // CTA 0: both CTAs' loads landed
+  uint64_t *empty = full + S::kStages;                  // per CTA: MMAs done with the stage
+  uint64_t *acc_full = empty + S::kStages;              // per CTA
   uint64_t *acc_empty = acc_full + 2;                       // CTA 0: both CTAs' epilogue warps
   uint64_t *drain = acc_empty + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
@@ -333,7 +346,7 @@ __global__ void __launch_bounds__(PairShape<PJ>::kThreads, 1)
   const int pair = static_cast<int>(blockIdx.x >> 1), n_pairs = static_cast<int>(gridDim.x >> 1);
   const int n_tiles = a.n_tt * a.n_jt;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < P_STAGES; ++s) {
+    for (int s = 0; s < S::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -345,6 +358,10 @@ __global__ void __launch_bounds__(PairShape<PJ>::kThreads, 1)
     fence_barrier_init();
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
+    int tt, jt;
+    pair_tile(pair, a.n_tt, a.n_jt, tt, jt);
+    for (int kb = 0; kb < S::kStages && kb < a.nkb; ++kb)
+      tma_prefetch_2d(&tmW, kb * PK, jt * PJ + static_cast<int>(rank) * (PJ / 2));
   }
   chain_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) reset_status(a.status);
@@ -380,14 +397,14 @@ __global__ void __launch_bounds__(PairShape<PJ>::kThreads, 1)
           tma_load_2d_pair(st + S::kX, &tmW, full0 + 8 * s, kb * PK, yw);
         }
         done |= 1u << s;
-        if (++s == P_STAGES) {
+        if (++s == S::kStages) {
           s = 0;
           ph ^= 1;
         }
       }
     }
     if (rank == 0) {  // the last loads of both CTAs have landed: stage q's was in this or the last lap
-      for (uint32_t q = 0; q < P_STAGES; ++q)
+      for (uint32_t q = 0; q < S::kStages; ++q)
         if ((done >> q & 1) && !mbar_wait_warp(&full[q], q < s ? ph ^ 1 : ph)) ok = false;
     }
     if (!ok && leader) set_status(a.status, kDevTimeout);
@@ -414,7 +431,7 @@ __global__ void __launch_bounds__(PairShape<PJ>::kThreads, 1)
             for (int kk = 1; kk < PK / 32; ++kk) mma_s8_pair(acc, dx + 2 * kk, dw + 2 * kk, idesc, 1u);
             mma_commit_pair(&empty[s], 3);
           }
-          if (++s == P_STAGES) {
+          if (++s == S::kStages) {
             s = 0;
             ph ^= 1;
           }
@@ -428,20 +445,23 @@ __global__ void __launch_bounds__(PairShape<PJ>::kThreads, 1)
     }
   } else {
     constexpr int BC = 64 / sizeof(T);            // outputs per staged box
-    const int ew = warp - 2, quarter = warp & 3, col0 = (ew >> 2) * S::kCols, c = threadIdx.x - 64;
-    uint8_t *stg = staging + ew * P_STAGING;
+    const int ew = warp - 2, quarter = warp & 3, col0 = (ew >> 2) * S::kCols;
+    uint8_t *stg = staging + ew * S::kStaging;
+    uint32_t stg_at = 0;
+    Cols &cl = cols[ew];
     auto load_ops = [&](int t) {
       TileOps o{};
       if (t >= n_tiles) return o;
-      int tt, jt;
-      pair_tile(t, a.n_tt, a.n_jt, tt, jt);
-      const int64_t j = static_cast<int64_t>(jt) * PJ + c;
-      if (c < PJ && j < a.d_out) {
-        o.ws = a.ws[j];
-        if (a.wz) o.wz = a.wz[j];
-        if (a.bias) o.bias = a.bias[j];
-      }
-      const int64_t row = static_cast<int64_t>(tt) * PT + half0 + quarter * 32 + lane;
+      pair_tile(t, a.n_tt, a.n_jt, o.tt, o.jt);
+      const int64_t j0 = static_cast<int64_t>(o.jt) * PJ + col0 + lane;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (j0 + 32 * i < a.d_out) {
+          o.ws[i] = a.ws[j0 + 32 * i];
+          if (a.wz) o.wz[i] = a.wz[j0 + 32 * i];
+          if (a.bias) o.bias[i] = a.bias[j0 + 32 * i];
+        }
+      const int64_t row = static_cast<int64_t>(o.tt) * PT + half0 + quarter * 32 + lane;
       if (row < a.n_tok) {
         o.xs = a.xs[row];
         if (a.wz) o.xsum = a.xsum[row];
@@ -452,18 +472,17 @@ __global__ void __launch_bounds__(PairShape<PJ>::kThreads, 1)
     uint32_t ch = 0;
     bool ok = true;
     for (int t = pair; t < n_tiles; t += n_pairs, ++ch) {
-      int tt, jt;
-      pair_tile(t, a.n_tt, a.n_jt, tt, jt);
       const uint32_t buf = ch & 1, use = ch >> 1;
       const TileOps ops = next;
-      Cols<PJ> &cl = cols[buf];
-      if (c < PJ) {
-        // (the other buffer may still be read: this one was last read before
-        // every warp passed the previous tile's barrier)
-        cl.s[c] = __half2float(__ushort_as_half(ops.ws));
-        cl.z[c] = ops.wz;
-        cl.b[c] = ops.bias;
+      const int tt = ops.tt, jt = ops.jt;
+      __syncwarp();        // all lanes have read the last tile's operands
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        cl.s[lane + 32 * i] = __half2float(__ushort_as_half(ops.ws[i]));
+        if (a.wz) cl.z[lane + 32 * i] = ops.wz[i];
+        if (a.bias) cl.b[lane + 32 * i] = ops.bias[i];
       }
+      __syncwarp();
       next = load_ops(t + n_pairs);
       const int64_t row0 = static_cast<int64_t>(tt) * PT + half0 + quarter * 32;
       // M and R: the next tile's go to L2 now; this tile's, 16-bit, come
@@ -477,28 +496,23 @@ __global__ void __launch_bounds__(PairShape<PJ>::kThreads, 1)
       if (a.m || a.r) {
         if (kEarly) load_mr(static_cast<int64_t>(jt) * PJ + col0);
         if (t + n_pairs < n_tiles) {
-          int t2, j2;
-          pair_tile(t + n_pairs, a.n_tt, a.n_jt, t2, j2);
-          const int64_t next_row = static_cast<int64_t>(t2) * PT + half0 + quarter * 32 + lane;
-          const int64_t jw = static_cast<int64_t>(j2) * PJ + col0;
+          const int64_t next_row = static_cast<int64_t>(next.tt) * PT + half0 + quarter * 32 + lane;
+          const int64_t jw = static_cast<int64_t>(next.jt) * PJ + col0;
           for (int64_t j = jw; next_row < a.n_tok && j < jw + S::kCols && j < a.d_out; j += 128 / sizeof(T)) {
             if (a.m) prefetch_l2(static_cast<const T *>(a.m) + next_row * a.d_out + j);
             if (a.r) prefetch_l2(static_cast<const T *>(a.r) + next_row * a.d_out + j);
           }
         }
       }
-      named_bar_sync(1, 32 * S::kWarps);
-      // (a warp whose wait gave up keeps meeting the others at the barrier)
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], use & 1));
-      if (!ok) continue;
+      ok = mbar_wait_warp(&acc_full[buf], use & 1);
+      if (!ok) break;
       tc_fence_after();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * PJ + col0;
       // (rolled: the options' code per 32 columns is large, and the warps
       // would wait for instructions)
 #pragma unroll 1
       for (int q = 0; q < S::kCols / 32; ++q) {
-        const int cq = col0 + q * 32;                              // column in the tile
-        const int64_t j0 = static_cast<int64_t>(jt) * PJ + cq;
+        const int64_t j0 = static_cast<int64_t>(jt) * PJ + col0 + q * 32;
         float v[32];
         tmem_ld32(taddr + q * 32, v);
         if (q == S::kCols / 32 - 1) {
@@ -506,42 +520,48 @@ __global__ void __launch_bounds__(PairShape<PJ>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(&acc_empty[buf], 0);
         }
-        scale32(a, cl.s + cq, cl.z + cq, cl.b + cq, ops.xs, ops.xsum, v);
+        scale32(a, cl.s + q * 32, cl.z + q * 32, cl.b + q * 32, ops.xs, ops.xsum, v);
         act_all(v, a.act);
-        auto box = [&](auto half) {
+        auto put_box = [&](auto half) {
           constexpr int H = decltype(half)::value;
           const int64_t jb = j0 + H * BC;
-          if (a.y_tma) {
-            if (lane == 0) bulk_wait_group_read0();                // the buffer's last box has left it
+          uint8_t *const box = stg + stg_at;
+          if (S::kBoxes == 2) stg_at ^= P_STAGING;
+          if (a.y_tma) {                                           // the buffer's last box has left it
+            if (lane == 0) {
+              if (S::kBoxes == 2) bulk_wait_group_read1();
+              else bulk_wait_group_read0();
+            }
             __syncwarp();
           }
           if (a.m) {
             if (!kEarly) m.load(a, a.m, row0, jb, lane);
-            m.to_row(stg, lane);
+            m.to_row(box, lane);
             m.template times<H>(v);
           }
           if (a.r) {
             if (!kEarly) r.load(a, a.r, row0, jb, lane);
-            r.to_row(stg, lane);
+            r.to_row(box, lane);
             r.template plus<H>(v);
           }
           if (kEarly && q + 1 < S::kCols / 32) load_mr(j0 + 32);
-          stage_row<H>(stg, lane, v, T());
+          stage_row<H>(box, lane, v, T());
           if (a.y_tma) {
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && jb < a.d_out && row0 < a.n_tok) {
-              tma_store_2d(&tmY, stg, static_cast<int32_t>(jb), static_cast<int32_t>(row0));
-              bulk_commit_group();
+            if (lane == 0) {
+              if (jb < a.d_out && row0 < a.n_tok)
+                tma_store_2d(&tmY, box, static_cast<int32_t>(jb), static_cast<int32_t>(row0));
+              bulk_commit_group();       // (an empty group too: the waits count them)
             }
           } else {
             __syncwarp();
-            store_box<T>(a, stg, lane, row0, jb);
+            store_box<T>(a, box, lane, row0, jb);
             __syncwarp();
           }
         };
-        box(std::integral_constant<int, 0>());
-        if constexpr (BC == 16) box(std::integral_constant<int, 1>());
+        put_box(std::integral_constant<int, 0>());
+        if constexpr (BC == 16) put_box(std::integral_constant<int, 1>());
       }
     }
     if (lane == 0) bulk_wait_group0();
@@ -662,6 +682,8 @@ __global__ void __launch_bounds__(F_THREADS)
     fence_barrier_init();
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
+    for (int it = 0; it < p.stages && it < nkb; ++it)
+      tma_prefetch_2d(&tmW, (kb0 + it) * PK, jt * F_J);
   }
   chain_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) reset_status(a.status);
@@ -795,7 +817,11 @@ __global__ void __launch_bounds__(F_THREADS)
 // steps in flight) straight from global memory and multiplies them with NT tokens by
 // dp4a; `ks` warps of a block share a row group along K and add up through
 // shared memory.  No barriers, no TMEM and no tensor maps to set up: the
-// weights' bytes and one memory round trip are all there is.
+// weights' bytes and one memory round trip are all there is.  HBM-bound: one
+// token 4096 -> 11008 9.8 us of 6.9 at the copy rate, 768 -> 2304 2.2 us.  The
+// first steps' weights start towards L2 before the stream's earlier work is
+// done (whose results they may be: nothing is read yet): behind a token's norm
+// 11.5 us instead of 12.3, 768 -> 2304 3.9 instead of 4.1.
 constexpr int V_R = 4, V_WARPS = 4;
 
 __device__ __forceinline__ int4 ld_stream(const int8_t *p) {
@@ -812,6 +838,9 @@ __global__ void __launch_bounds__(V_WARPS * 32) w8a8_vec_kernel(W8Args a, int ks
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = V_WARPS / ks, kp = warp % ks, grp = warp / ks;
   const int64_t j0 = (static_cast<int64_t>(blockIdx.x) * groups + grp) * V_R;
+  constexpr int ST = NT == 1 ? 4 : 2;   // steps in flight
+  if (kp == 0 && lane < V_R && j0 + lane < a.d_out)
+    prefetch_l2(a.w + (j0 + lane) * a.d_in, a.d_in < ST * ks * 512 ? a.d_in : ST * ks * 512);
   chain_wait();
   chain_next();
   if (blockIdx.x == 0 && threadIdx.x == 0) reset_status(a.status);
@@ -820,7 +849,6 @@ __global__ void __launch_bounds__(V_WARPS * 32) w8a8_vec_kernel(W8Args a, int ks
 #pragma unroll
   for (int r = 0; r < V_R; ++r)  // rows past the end read the last one again
     w[r] = a.w + (j0 + r < a.d_out ? j0 + r : a.d_out - 1) * a.d_in;
-  constexpr int ST = NT == 1 ? 4 : 2;   // steps in flight
   const int stride = ks * 512;
   for (int k = kp * 512 + lane * 16; k < a.d_in; k += ST * stride) {
     int4 wv[ST][V_R], xv[ST][NT];
