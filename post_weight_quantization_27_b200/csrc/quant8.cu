@@ -61,11 +61,11 @@ struct Factors {
   uint64_t f[P];
   template <typename WT>
   __device__ __forceinline__ void load(const WT *w) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(w));
+    const uint4 a = *reinterpret_cast<const uint4 *>(w);
     if constexpr (sizeof(WT) == sizeof(T)) {
       widen(a, f, T());
     } else {
-      const uint4 b = __ldg(reinterpret_cast<const uint4 *>(w) + 1);
+      const uint4 b = *(reinterpret_cast<const uint4 *>(w) + 1);
       set(0, a);
       set(1, b);
     }
@@ -108,6 +108,16 @@ __device__ __forceinline__ uint32_t narrow2(uint64_t v, __nv_bfloat16) {
 template <typename T>
 __device__ __forceinline__ uint4 narrow(const uint64_t (&v)[4], T t) {
   return make_uint4(narrow2(v[0], t), narrow2(v[1], t), narrow2(v[2], t), narrow2(v[3], t));
+}
+
+// 16 bytes that are read once (volatile, so that no load leaves its place
+// behind chain_wait, as one that the compiler takes for a function of its
+// address might).
+__device__ __forceinline__ uint4 load16_once(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
 }
 
 // The larger of a and |b|, |c|; NaN when one is NaN.
@@ -381,8 +391,8 @@ __global__ void __launch_bounds__(N == 8 ? 1024 : 256, N == 8 ? 1 : 3) quant_blo
   for (int v = 0; v < U; ++v) {
     const int c = c0 + v * cs;
     if (c < c1) {
-      xr[v] = __ldcs(reinterpret_cast<const uint4 *>(x + c));
-      if (res) rr[v] = __ldcs(reinterpret_cast<const uint4 *>(r + c));
+      xr[v] = load16_once(x + c);
+      if (res) rr[v] = load16_once(r + c);
     }
   }
   uint64_t g[U][E / 2];

@@ -828,7 +828,8 @@ __device__ __forceinline__ int4 ld_stream(const int8_t *p) {
   int4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "l"(p)
+               : "memory");
   return v;
 }
 
@@ -869,7 +870,7 @@ __global__ void __launch_bounds__(V_WARPS * 32) w8a8_vec_kernel(W8Args a, int ks
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         xv[u][t] = ku < a.d_in
-                       ? __ldg(reinterpret_cast<const int4 *>(a.x + static_cast<int64_t>(t) * a.d_in + ku))
+                       ? *reinterpret_cast<const int4 *>(a.x + static_cast<int64_t>(t) * a.d_in + ku)
                        : make_int4(0, 0, 0, 0);
     }
 #pragma unroll
