@@ -143,10 +143,13 @@ __device__ __forceinline__ bool mbar_wait_cluster_warp(uint64_t *bar, uint32_t p
 
 // Chained launches (launch_chained): chain_wait returns when the stream's
 // earlier work has completed and its memory is visible; every thread of such
-// a kernel calls it before its first access to global memory, so that a
-// kernel has completed only after everything before it.  chain_next lets the
-// next chained launch's blocks start and set themselves up; a kernel calls
-// it when its blocks hold the tensor memory that they need.
+// a kernel calls it before it reads or writes global memory (requests to
+// bring lines to L2 read nothing), so that a kernel has completed only after
+// everything before it.  Such a kernel may start while its operands are still
+// being written: it reads none of them by ld.global.nc, which is for memory
+// that stays the same while a kernel runs.  chain_next lets the next chained
+// launch's blocks start and set themselves up; a kernel calls it when its
+// blocks hold the tensor memory that they need.
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void chain_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

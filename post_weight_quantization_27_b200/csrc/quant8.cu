@@ -367,7 +367,10 @@ __device__ __forceinline__ int put(uint64_t (&g)[P], const RowGrid &gr, int8_t *
 // N = 8 for a few tokens: the time is one load's latency, the reductions and
 // the launch (one token of 4096: 1.9 us in a graph, 2.6 with residual and
 // norm).  N = 32 while the rows fit the SMs at once, and for rows that the
-// persistent kernel cannot hold.
+// persistent kernel cannot hold (16 elements per thread were 4 to 13% faster
+// around 4M elements and slower on both sides of that: not kept).  Measured
+// (bf16, graph replays): 150 x 768, N = 8, plain 1.5 us, norm 2.0; N = 32: 512
+// x 4096 plain 3.3 us, norm 5.3, 100 x 28672 norm with residual 8.2 us.
 constexpr int kSlice = 8192;
 
 template <typename T, typename WT, Mode MODE, int N>
@@ -444,17 +447,23 @@ __global__ void __launch_bounds__(N == 8 ? 1024 : 256, N == 8 ? 1 : 3) quant_blo
 // Persistent blocks, 32 elements per thread: `team` threads take a row at a
 // time, always the same columns, whose factors stay on the SM as fp32: in
 // shared memory (the copies of a thread's own columns, 16 bytes a lane: no
-// bank conflicts, no misses behind the stream of rows), or, for fp32 rows of
-// up to 20480 elements, in registers (WREG: such rows need few instructions
-// per byte, so fewer threads are enough; 134M elements with column factors
-// 104 against 140 us).  Each thread copies its own units of
-// the rows ahead into a ring of its own there (cp.async, AHEAD rows), so
-// loads go on while a row is reduced and written, no registers wait for them
-// and no thread waits for another's copies; a row is read once and stays in
-// registers between the statistics and the codes, both of which take g from
-// it (g itself would be twice the registers, and spill).  One barrier per row: the codes' sums of a row
-// are added up behind the next row's.  HBM-bound: x (and r) read, codes (and
-// h) written.
+// bank conflicts, no misses behind the stream of rows: 43 to 57% of the copy
+// bandwidth when they came through L1), or, for fp32 rows of up to 20480
+// elements, in registers (WREG: such rows need few instructions per byte, so
+// fewer threads are enough; 134M elements with column factors 104 against
+// 140 us).  Each thread copies its own units of the rows ahead into a ring of
+// its own there (cp.async, AHEAD rows), so loads go on while a row is reduced
+// and written, no registers wait for them and no thread waits for another's
+// copies; a row is read once and stays in registers between the statistics
+// and the codes, both of which take g from it (g itself would be twice the
+// registers, and spill: 54% of the copy bandwidth instead of 77% when it was
+// tried).  One barrier per row: the codes' sums of a row are added up behind
+// the next row's.  x (and r) are read, codes (and h) written: plain rows and
+// fp32 rows are bound by HBM (16384 x 28672 bf16 204 us = 105% of the copy
+// bandwidth, 16384 x 8192 fp32 with factors 104 us = 99%), 16-bit rows with
+// factors also by the instructions issued, about 16 an element with column
+// factors and 21 with the norm against 11 plain (16384 x 28672 263 us = 82%,
+// 32768 x 8192 norm with residual 306 us = 94%, without 216 us = 57%).
 constexpr int kRegThreads = 640;
 constexpr size_t kRingMost = 225 * 1024;
 __device__ __forceinline__ void cp_async16(uint32_t dst, const char *src) {
@@ -706,7 +715,7 @@ gq_status launch_rows(QuantArgs a, cudaStream_t st) {
   return launched(e, "quant kernel");
 }
 
-// 16 codes per thread from the packed bit stream.
+// 16 codes per thread from the packed bit stream (once per layer).
 __global__ void __launch_bounds__(256)
     unpack8_kernel(const uint32_t *q, const uint16_t *zeros, int64_t d_out, int64_t d_in, int bits,
                    int8_t *codes, int32_t *zpoint) {

@@ -536,6 +536,65 @@ def test_calls_behind_one_another_see_each_others_results(n):
         assert all(torch.equal(a, b) for a, b in zip(ref, got))
 
 
+@pytest.mark.parametrize("n", [1, 6, 40, 300])
+def test_calls_behind_copies_and_other_streams(n):
+    """The same behind what is not a kernel (copies from the host and on the device, clearing) and
+    behind a stream that joins, at once and captured into a graph."""
+    d = 512
+    w, w2, _ = _mlp_layers(d, d)
+    host = [_x(n, d, "bf16", seed=i).pin_memory() for i in range(4)]
+    x, src = torch.zeros(n, d, dtype=torch.bfloat16, device="cuda"), host[3].cuda()
+    y, z, t = torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(x)
+    tok, tok2 = gq.quantize_tokens_int8(x), gq.quantize_tokens_int8(x)
+    side = torch.cuda.Stream()
+
+    def calls():
+        x.copy_(src, non_blocking=True)
+        gq.quantize_tokens_int8(x, out=tok)
+        z.zero_()
+        gq.w8a8_matmul(w, tok, R=z, Y=y)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            gq.quantize_tokens_int8(y, out=tok2)
+            gq.w8a8_matmul(w2, tok2, Y=t)
+        z.copy_(y)
+        gq.w8a8_matmul(w, tok, act="silu", mul=z, Y=z)
+        torch.cuda.current_stream().wait_stream(side)
+        gq.rmsnorm_quantize_int8(t, torch.ones(d, device="cuda"), R=z, H=z, out=tok)
+        gq.w8a8_matmul(w2, tok, R=z, Y=t)
+
+    def expect(xh):
+        k = gq.quantize_tokens_int8(xh.cuda())
+        torch.cuda.synchronize()
+        y_ = gq.w8a8_matmul(w, k, R=torch.zeros_like(x))
+        torch.cuda.synchronize()
+        k2 = gq.quantize_tokens_int8(y_)
+        torch.cuda.synchronize()
+        t_ = gq.w8a8_matmul(w2, k2)
+        z_ = gq.w8a8_matmul(w, k, act="silu", mul=y_)
+        torch.cuda.synchronize()
+        q = gq.rmsnorm_quantize_int8(t_, torch.ones(d, device="cuda"), R=z_)
+        torch.cuda.synchronize()
+        out = gq.w8a8_matmul(w2, q, R=q["h"])
+        torch.cuda.synchronize()
+        return out
+    ref = [expect(h) for h in host]
+    for i in range(12):
+        src.copy_(host[i % 4], non_blocking=True)
+        calls()
+        torch.cuda.synchronize()
+        assert torch.equal(t, ref[i % 4])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    for i in range(12):
+        src.copy_(host[i % 4], non_blocking=True)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(t, ref[i % 4])
+    del g
+
+
 def test_results_do_not_change_from_run_to_run():
     w1, _, w3 = _mlp_layers(1024, 1536)
     for n in (1, 24, 200, 600):
