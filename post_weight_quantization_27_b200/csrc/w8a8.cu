@@ -6,6 +6,7 @@
 // difference sum x (c - zpoint) at most 128 * 255 * 65536 < 2^31.  One
 // rounding takes it to fp32, where the epilogue works, and one more to the
 // output's type.
+#include <cfloat>
 #include <type_traits>
 
 #include "gq_device.cuh"
@@ -28,8 +29,6 @@ struct W8Args {
   int act;
   int *status;
   int n_tt, n_jt, nkb;    // tiles of tokens, tiles of outputs, K steps
-  int y_vec;              // rows of Y, M and R are a multiple of 16 bytes long
-  int y_tma;              // .. and Y leaves by TMA
 };
 
 // acc - z xsum in two's complement.
@@ -174,7 +173,7 @@ __device__ __forceinline__ void prefetch_l2(const void *p, int bytes) {  // mult
 __device__ __forceinline__ int box_at(int r, int c) {   // 16-byte chunk c of row r
   return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
-template <typename T>
+template <typename T, bool WHOLE>
 struct Box {
   static constexpr int E = 16 / static_cast<int>(sizeof(T));
   uint4 u[4];
@@ -185,7 +184,7 @@ struct Box {
 #pragma unroll
     for (int i = 0; i < 4; ++i, p += 8 * a.d_out) {
       if (row0 + (lane >> 2) + 8 * i >= a.n_tok) break;
-      if (a.y_vec) {
+      if constexpr (WHOLE) {
         if (j < a.d_out) u[i] = *reinterpret_cast<const uint4 *>(p);
       } else {
 #pragma unroll
@@ -246,18 +245,67 @@ __device__ __forceinline__ void stage_row(uint8_t *stg, int r, const float (&v)[
     *reinterpret_cast<uint4 *>(stg + box_at(r, c)) = u;
   }
 }
-// A staged box to Y with ordinary stores: half a row (16-bit: a row) per
-// 16 (32) lanes.
+// 64 fp32 outputs of R tokens from shared memory (before M and R) to Y, where
+// rows of Y, M and R are no multiple of 16 bytes long: M, R and Y at the same
+// addresses, row after row.  A row's pieces follow one another, so that the
+// sectors that two of them share are written whole: the stores of 2048 rows of
+// 50257 alone take 99 us so and 230 in boxes of 16 outputs (65 where sectors
+// are whole).
+constexpr int kRowPitch = 68;                  // floats (no bank conflicts)
+template <int R>
+__device__ __forceinline__ void put_rows(const W8Args &a, const float *stg, int64_t at, int rows,
+                                         int n, int lane) {
+  float *y = static_cast<float *>(a.y) + at + lane;
+  const float *mp = static_cast<const float *>(a.m) + at + lane;
+  const float *rp = static_cast<const float *>(a.r) + at + lane;
+  const int live[2] = {lane < n ? rows : 0, lane + 32 < n ? rows : 0};
+#pragma unroll
+  for (int r0 = 0; r0 < R; r0 += 4) {
+    float v[4][2], u[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v[i][h] = stg[(r0 + i) * kRowPitch + h * 32 + lane];
+    if (a.m) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (r0 + i < live[h]) u[i][h] = mp[(r0 + i) * a.d_out + h * 32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) v[i][h] *= u[i][h];
+    }
+    if (a.r) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (r0 + i < live[h]) u[i][h] = rp[(r0 + i) * a.d_out + h * 32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) v[i][h] += u[i][h];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (r0 + i < live[h]) y[(r0 + i) * a.d_out + h * 32] = v[i][h];
+  }
+}
+// A staged box of 16-bit outputs to such rows: a row per store, 32 lanes.
+// (Rows of 64 in 4-byte stores, a lane's pair by its row's parity, took 253 us
+// instead of 160 for 2048 rows of 50257 behind 768 inputs: more instructions.)
 template <typename T>
 __device__ __forceinline__ void store_box(const W8Args &a, const uint8_t *stg, int lane,
                                           int64_t row0, int64_t j0) {
-  constexpr int BC = 64 / sizeof(T), E = 16 / sizeof(T), RS = 32 / BC;   // rows per step
-  const int c = lane % BC;
-  T *y = static_cast<T *>(a.y) + row0 * a.d_out + j0 + c;
+  T *y = static_cast<T *>(a.y) + row0 * a.d_out + j0 + lane;
   const int rows = a.n_tok - row0 < 32 ? static_cast<int>(a.n_tok - row0) : 32;
-  if (j0 + c >= a.d_out) return;
-  for (int r = lane / BC; r < rows; r += RS)
-    y[r * a.d_out] = *reinterpret_cast<const T *>(stg + box_at(r, c / E) + (c % E) * sizeof(T));
+  if (j0 + lane >= a.d_out) return;
+  for (int r = 0; r < rows; ++r)
+    y[r * a.d_out] = *reinterpret_cast<const T *>(stg + box_at(r, lane / 8) + (lane % 8) * 2);
 }
 
 // ---------------------------------------------------------------- many tokens
@@ -293,7 +341,7 @@ struct Cols {              // operands of an epilogue warp's outputs, in shared 
   int z[64];
   float b[64];
 };
-template <int PJ>
+template <int PJ, bool TMA>
 struct PairShape {
   static constexpr int kStages = PJ == 256 ? 5 : 7;
   static constexpr int kBoxes = PJ == 256 ? 1 : 2;       // staged boxes per epilogue warp
@@ -302,7 +350,10 @@ struct PairShape {
   static constexpr int kWarps = PJ / 16;                 // of the epilogue
   static constexpr int kCols = 64;                       // outputs of each of its warps
   static constexpr int kThreads = 64 + 32 * kWarps;
-  static constexpr int kStaging = kBoxes * P_STAGING;
+  static constexpr int kRows = 16;                       // .. or rows of put_rows (PJ = 128)
+  static constexpr int kStaging = PJ == 256 ? P_STAGING : 4608;
+  static_assert(kBoxes * P_STAGING <= kStaging && (PJ == 256 || kRows * kRowPitch * 4 <= kStaging) &&
+                    kStaging % 512 == 0, "what is staged fits, boxes on the swizzle's period");
   static constexpr size_t kSmem = 1024 + kStages * kStage + kWarps * (kStaging + sizeof(Cols)) + 256;
 };
 struct TileOps {           // what one thread brings for a tile: two outputs' operands, its token's
@@ -323,12 +374,13 @@ __device__ __forceinline__ void pair_tile(int t, int n_tt, int n_jt, int &tt, in
   jt = r / rows;
 }
 
-template <typename T, int PJ>
-__global__ void __launch_bounds__(PairShape<PJ>::kThreads, 1)
+// TMA: rows of Y, M and R are a multiple of 16 bytes long.
+template <typename T, int PJ, bool TMA>
+__global__ void __launch_bounds__(PairShape<PJ, TMA>::kThreads, 1)
     w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX,
                      const __grid_constant__ CUtensorMap tmW,
                      const __grid_constant__ CUtensorMap tmY, W8Args a) {
-  using S = PairShape<PJ>;
+  using S = PairShape<PJ, TMA>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -488,7 +540,7 @@ __global__ void __launch_bounds__(PairShape<PJ>::kThreads, 1)
       // M and R: the next tile's go to L2 now; this tile's, 16-bit, come
       // before the sums are needed, fp32, twice the registers, when they are
       constexpr bool kEarly = sizeof(T) == 2;
-      Box<T> m, r;
+      Box<T, TMA> m, r;
       auto load_mr = [&](int64_t j) {
         if (a.m) m.load(a, a.m, row0, j, lane);
         if (a.r) r.load(a, a.r, row0, j, lane);
@@ -508,6 +560,39 @@ __global__ void __launch_bounds__(PairShape<PJ>::kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * PJ + col0;
+      if constexpr (!TMA && sizeof(T) == 4) {
+        float v[2][32];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          tmem_ld32(taddr + q * 32, v[q]);
+          if (q == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(&acc_empty[buf], 0);
+          }
+          scale32(a, cl.s + q * 32, cl.z + q * 32, cl.b + q * 32, ops.xs, ops.xsum, v[q]);
+          act_all(v[q], a.act);
+        }
+        constexpr int R = S::kRows;                                // rows that the buffer holds
+        float *rows = reinterpret_cast<float *>(stg);
+        const int64_t j0 = static_cast<int64_t>(jt) * PJ + col0, left = a.n_tok - row0;
+        const int n = a.d_out - j0 < 64 ? static_cast<int>(a.d_out - j0) : 64;
+#pragma unroll 1
+        for (int p = 0; p < 32; p += R) {
+          if (lane / R == p / R) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float *u = &v[c / 8][c % 8 * 4];
+              *reinterpret_cast<float4 *>(rows + lane % R * kRowPitch + 4 * c) = make_float4(u[0], u[1], u[2], u[3]);
+            }
+          }
+          __syncwarp();
+          if (n > 0 && left > p)
+            put_rows<R>(a, rows, (row0 + p) * a.d_out + j0, left - p < R ? static_cast<int>(left - p) : R, n, lane);
+          __syncwarp();
+        }
+        continue;
+      }
       // (rolled: the options' code per 32 columns is large, and the warps
       // would wait for instructions)
 #pragma unroll 1
@@ -527,7 +612,7 @@ __global__ void __launch_bounds__(PairShape<PJ>::kThreads, 1)
           const int64_t jb = j0 + H * BC;
           uint8_t *const box = stg + stg_at;
           if (S::kBoxes == 2) stg_at ^= P_STAGING;
-          if (a.y_tma) {                                           // the buffer's last box has left it
+          if constexpr (TMA) {                                     // the buffer's last box has left it
             if (lane == 0) {
               if (S::kBoxes == 2) bulk_wait_group_read1();
               else bulk_wait_group_read0();
@@ -546,7 +631,7 @@ __global__ void __launch_bounds__(PairShape<PJ>::kThreads, 1)
           }
           if (kEarly && q + 1 < S::kCols / 32) load_mr(j0 + 32);
           stage_row<H>(box, lane, v, T());
-          if (a.y_tma) {
+          if constexpr (TMA) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -600,7 +685,7 @@ struct FewPlan {
   int bn;            // tokens per tile, a multiple of 16
   int stages, split;
   int tmem_cols;
-  int steps;         // K steps on the fullest SM
+  int steps, held;   // K steps and CTAs on the fullest SM
 };
 
 __device__ __forceinline__ int ld_cluster_s32(uint32_t cluster_addr) {
@@ -918,30 +1003,42 @@ constexpr CUtensorMapDataType tmap_type() {
   return sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 }
 
-template <typename T, int PJ>
-gq_status launch_pair(W8Args a, cudaStream_t st) {
-  using S = PairShape<PJ>;
+template <typename T, int PJ, bool TMA>
+gq_status launch_pair_as(W8Args a, cudaStream_t st) {
+  using S = PairShape<PJ, TMA>;
   static SmemOptIn opt;
   CUtensorMap tX, tW, tY{};
   gq_status s = make_tmap_2d(&tX, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.d_in, a.n_tok, a.d_in, PK, 128);
   if (s == GQ_OK)
     s = make_tmap_2d(&tW, a.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.d_in, a.d_out, a.d_in, PK, PJ / 2);
-  if (s == GQ_OK && a.y_vec)
+  if (s == GQ_OK && TMA)
     s = make_tmap_2d(&tY, a.y, tmap_type<T>(), sizeof(T), a.d_out, a.n_tok, a.d_out, 64 / sizeof(T),
                      32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (s != GQ_OK) return s;
-  a.y_tma = a.y_vec;
   a.n_tt = static_cast<int>((a.n_tok + PT - 1) / PT);
   a.n_jt = static_cast<int>((a.d_out + PJ - 1) / PJ);
   a.nkb = (a.d_in + PK - 1) / PK;
   const int tiles = a.n_tt * a.n_jt, pairs = num_sms() / 2;
-  opt.allow(w8a8_pair_kernel<T, PJ>, S::kSmem);
+  opt.allow(w8a8_pair_kernel<T, PJ, TMA>, S::kSmem);
   const int slot = timer_begin(GQ_KERNEL_W8A8, st);
-  const cudaError_t e = launch_chained(w8a8_pair_kernel<T, PJ>, 2 * (tiles < pairs ? tiles : pairs),
+  const cudaError_t e = launch_chained(w8a8_pair_kernel<T, PJ, TMA>, 2 * (tiles < pairs ? tiles : pairs),
                                        S::kThreads, S::kSmem, st, 2, tX, tW, tY, a);
   count_launch();
   timer_end(slot, st, 2.0 * static_cast<double>(a.n_tok) * a.d_out * a.d_in);
   return launched(e, "w8a8_pair_kernel");
+}
+
+// Whether rows of Y (and of M and R) are a multiple of 16 bytes long.
+template <typename T>
+bool whole_rows(const W8Args &a) {
+  return a.d_out * sizeof(T) % 16 == 0;
+}
+template <typename T, int PJ>
+gq_status launch_pair(const W8Args &a, cudaStream_t st) {
+  if constexpr (sizeof(T) == 4 && PJ == 256)          // (ragged fp32 rows: 128 or few tiles)
+    return launch_pair_as<T, PJ, true>(a, st);
+  else
+    return whole_rows<T>(a) ? launch_pair_as<T, PJ, true>(a, st) : launch_pair_as<T, PJ, false>(a, st);
 }
 
 // CTAs per tile: the split whose fullest SM has the fewest K steps, the
@@ -964,6 +1061,9 @@ FewPlan few_plan(int64_t n_tok, int64_t d_out, int nkb, int &n_tt, int &n_jt) {
   for (int c = 1; c <= 8 && (c == 1 || nkb >= 4 * c); ++c) {
     const int64_t held = (tiles * c + sms - 1) / sms;
     if (c > 1 && held > 2) break;
+    // (larger clusters do not fill the last SMs: 384 x 4096 x 4096 in threes,
+    // 288 CTAs in 296 places, 30 us, unsplit 15)
+    if (c > 2 && 10 * tiles * c > 9 * held * sms) continue;
     const int64_t cost = held * ((nkb + c - 1) / c);
     if (cost < best) {
       best = cost;
@@ -972,6 +1072,7 @@ FewPlan few_plan(int64_t n_tok, int64_t d_out, int nkb, int &n_tt, int &n_jt) {
     }
   }
   p.steps = static_cast<int>(best < INT32_MAX ? best : INT32_MAX);
+  p.held = static_cast<int>(per_sm < INT32_MAX ? per_sm : INT32_MAX);
   const int stage = (F_J + p.bn) * PK;
   const int kb = per_sm == 1 ? 216 : per_sm == 2 ? 108 : 72;
   p.stages = kb * 1024 / stage;
@@ -1033,41 +1134,60 @@ gq_status launch_vec(const W8Args &a, cudaStream_t st) {
   }
 }
 
-// Expected microseconds of a pair kernel: launch and first loads, a round of
-// tiles per 74 pairs, each bound by its MMAs or by its epilogue (rows of Y
-// that TMA cannot store, fp32), and the last epilogue.  Steps of 0.35 (PJ =
-// 256) and 0.25 us (128) as measured: an N = 128 MMA reads its A tile twice
-// as often per flop.
+// Expected microseconds of a pair kernel: launch and first loads, the first
+// tile's MMAs, a round of tiles per 74 pairs, each bound by its MMAs or by its
+// epilogue, and the last epilogue.  Steps of 0.35 (PJ = 256) and 0.23 us (128):
+// an N = 128 MMA reads its A tile twice as often per flop.
 template <typename T, int PJ>
 float pair_us(const W8Args &a, int nkb) {
   const int64_t tiles = ((a.n_tok + PT - 1) / PT) * ((a.d_out + PJ - 1) / PJ), pairs = num_sms() / 2;
   const float rounds = static_cast<float>((tiles + pairs - 1) / pairs);
-  const float epi = (PJ == 256 ? 3.0f : 2.0f) * (sizeof(T) == 4 ? 1.7f : 1.0f) * (a.y_vec ? 1.0f : 1.7f);
-  const float mma = static_cast<float>(nkb) * (PJ == 256 ? 0.35f : 0.25f);
-  return 5.5f + rounds * (mma > epi ? mma : epi) + epi;
+  const bool whole = whole_rows<T>(a), wide = PJ == 256;
+  if (!whole && wide && sizeof(T) == 4) return FLT_MAX;
+  const float epi = sizeof(T) == 4 ? (whole ? (wide ? 4.7f : 3.2f) : 4.0f)
+                                   : (whole ? (wide ? 3.8f : 2.5f) : (wide ? 5.5f : 3.8f));
+  const float mma = static_cast<float>(nkb) * (wide ? 0.35f : 0.23f);
+  return 3.5f + mma + (rounds - 1.0f) * (mma > epi ? mma : epi) + epi;
+}
+// Of the kernel for few tiles: launch and first loads, the weights from HBM or
+// the fullest SM's steps, and the epilogues (of tiles that share an SM they
+// overlap in part; a split tile's sums are exchanged first).
+float few_us(const W8Args &a, const FewPlan &p) {
+  const float bn = static_cast<float>(p.bn);
+  const float hbm = static_cast<float>(a.d_out) * static_cast<float>(a.d_in) / 6.5e6f;
+  const float steps = static_cast<float>(p.steps) * (F_J + bn) * PK / 140e3f;
+  return 3.5f + (hbm > steps ? hbm : steps) +
+         (p.split > 1 ? 1.5f + 0.06f * bn : 0.035f * bn * (1.0f + 0.45f * static_cast<float>(p.held - 1)));
 }
 
-// The kernel is chosen by these estimates.  Measured (us, graph replays, bf16
-// out, one per call below the line taken):
-//   n   d_in  d_out    vec   few   256   128
-//   4   2048   8192    6.4   8.7     -     -
-//   8   2048   8192    9.7   8.8     -     -
-//   33  8192   8192      -  19.2  27.3  20.6
-//   48  4096  11008      -  15.3  18.9  19.0
-//   256 8192   8192      -  25.3  28.4  21.9
-//   512 8192   8192      -  35.2  29.2  31.5
-//  2048 4096  11008      -     -  62.6  69.1
+// The kernel is chosen by these estimates; dp4a for one token, and for up to
+// eight while the layer is small and its products few.  Measured (us, graph
+// replays, weights from HBM, bf16 out; fp32 in the last two lines):
+//   n    d_in   d_out    dp4a   few   256   128
+//   1    4096   11008     9.6  11.8  23.6  24.4
+//   1    28672  8192     36.6  40.9  82.2  88.7
+//   2    8192   8192     17.8  16.5  27.8  29.2
+//   4    4096   11008    11.3  11.8  22.1  22.3
+//   8    4096   4096      5.9   8.5  15.6  12.8
+//   8    4096   11008    14.8  11.9  21.0  20.9
+//   33   8192   28672       -  44.9  54.5  58.1
+//   64   8192   8192        -  19.8  27.3  20.1
+//   256  8192   8192        -  24.2  27.9  20.9
+//   384  4096   11008       -  22.3  27.7  24.7
+//   512  8192   8192        -  34.1  28.6  31.1
+//   512  4096   11008       -  29.9  28.3  25.2
+//   2048 4096   11008       - 100.4  62.8  69.2
+//   251  768    50257       -  28.3     -  29.8
+//   2048 2048   8191        -  51.5     -  38.7
 template <typename T>
 gq_status launch_typed(W8Args a, cudaStream_t st) {
-  a.y_vec = a.d_out * sizeof(T) % 16 == 0;
-  if (a.n_tok <= 3 || (a.n_tok <= 8 && a.n_tok * a.d_in * a.d_out < (int64_t(1) << 27)))
+  const int64_t layer = a.d_in * a.d_out;
+  if (a.n_tok == 1 || (a.n_tok <= 8 && layer < (int64_t(3) << 24) && a.n_tok * layer < (int64_t(3) << 26)))
     return launch_vec<T>(a, st);
   W8Args f = a;
   f.nkb = (a.d_in + PK - 1) / PK;
   const FewPlan p = few_plan(a.n_tok, a.d_out, f.nkb, f.n_tt, f.n_jt);
-  // a CTA's loads arrive at about 50 GB/s; an unsplit SM's epilogues overlap
-  const float few = 5.0f + static_cast<float>(p.steps) * static_cast<float>((F_J + p.bn) * PK) / 50e3f +
-                    (p.split > 1 ? 1.5f : 0.0f) + 0.035f * static_cast<float>(p.bn);
+  const float few = few_us(a, p);
   const float wide = pair_us<T, 256>(a, f.nkb), narrow = pair_us<T, 128>(a, f.nkb);
   if (few <= wide && few <= narrow) return launch_few<T>(f, p, st);
   return wide <= narrow ? launch_pair<T, 256>(a, st) : launch_pair<T, 128>(a, st);
@@ -1085,7 +1205,7 @@ gq_status launch_w8a8(const int8_t *w_codes, const uint16_t *w_scales, const int
     return check_launch("memset");
   }
   const W8Args a{w_codes, x_codes, w_scales, w_zpoint, x_scales, x_sums, bias, M, R, Y,
-                 d_out,   n_tok,   static_cast<int>(d_in), act, status, 0, 0, 0, 0, 0};
+                 d_out,   n_tok,   static_cast<int>(d_in), act, status, 0, 0, 0};
   switch (y_dtype) {
     case GQ_F32: return launch_typed<float>(a, st);
     case GQ_F16: return launch_typed<__half>(a, st);
