@@ -29,6 +29,7 @@ struct W8Args {
   int act;
   int *status;
   int n_tt, n_jt, nkb;    // tiles of tokens, tiles of outputs, K steps
+  int pj;                 // outputs of a pair's tile
 };
 
 // acc - z xsum in two's complement.
@@ -309,8 +310,8 @@ __device__ __forceinline__ void store_box(const W8Args &a, const uint8_t *stg, i
 }
 
 // ---------------------------------------------------------------- many tokens
-// 256 (tokens) x PJ = 256 or 128 (outputs) tiles on CTA pairs (tcgen05
-// cta_group::2, kind::i8), persistent, K in steps of 128 bytes:
+// Tiles of 256 tokens x PJ = 256 (or 224: a.pj) or 128 outputs on CTA pairs
+// (tcgen05 cta_group::2, kind::i8), persistent, K in steps of 128 bytes:
 //   warp 0      TMA: CTA r of the pair stages the tile's token rows 128 r ..
 //               and output rows PJ / 2 r .., both CTAs' loads completing on
 //               CTA 0's full[s]
@@ -321,8 +322,8 @@ __device__ __forceinline__ void store_box(const W8Args &a, const uint8_t *stg, i
 //               token: the outputs' scales, zero-points and bias pass through
 //               shared memory of the warp's own, loaded a tile ahead; results
 //               pass a 64-byte-swizzled buffer of the warp's own and leave
-//               by TMA store (by coalesced stores where Y's rows are no
-//               multiple of 16 bytes).  No warp waits for another one's tile
+//               by TMA store; where Y's rows are no multiple of 16 bytes
+//               (!TMA), by ordinary ones.  No warp waits for another one's tile
 //               (operands shared by a barrier of all: 2560 x 2048 x 8192 with
 //               GELU 42.7 us, so 40.5).
 // The issuing warps' lanes walk their loops together, so that a step's values
@@ -374,7 +375,8 @@ __device__ __forceinline__ void pair_tile(int t, int n_tt, int n_jt, int &tt, in
   jt = r / rows;
 }
 
-// TMA: rows of Y, M and R are a multiple of 16 bytes long.
+// TMA: rows of Y, M and R are a multiple of 16 bytes long (kernels of their
+// own: 2048 x 768 x 50256 103 us with one kernel for both, so 93).
 template <typename T, int PJ, bool TMA>
 __global__ void __launch_bounds__(PairShape<PJ, TMA>::kThreads, 1)
     w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX,
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(PairShape<PJ, TMA>::kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = static_cast<int>(blockIdx.x >> 1), n_pairs = static_cast<int>(gridDim.x >> 1);
-  const int n_tiles = a.n_tt * a.n_jt;
+  const int n_tiles = a.n_tt * a.n_jt, pj = PJ == 256 ? a.pj : PJ;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(PairShape<PJ, TMA>::kThreads, 1)
     int tt, jt;
     pair_tile(pair, a.n_tt, a.n_jt, tt, jt);
     for (int kb = 0; kb < S::kStages && kb < a.nkb; ++kb)
-      tma_prefetch_2d(&tmW, kb * PK, jt * PJ + static_cast<int>(rank) * (PJ / 2));
+      tma_prefetch_2d(&tmW, kb * PK, jt * pj + static_cast<int>(rank) * (pj / 2));
   }
   chain_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) reset_status(a.status);
@@ -435,16 +437,17 @@ __global__ void __launch_bounds__(PairShape<PJ, TMA>::kThreads, 1)
     const bool leader = elect_one();
     bool ok = true;
     uint32_t s = 0, ph = 1, done = 0;
+    const uint32_t bytes = 2 * (S::kX + pj / 2 * PK);
     const uint32_t base = smem_u32(smem), full0 = mapa_shared(smem_u32(full), 0);
     for (int t = pair; t < n_tiles && ok; t += n_pairs) {
       int tt, jt;
       pair_tile(t, a.n_tt, a.n_jt, tt, jt);
-      const int yx = tt * PT + half0, yw = jt * PJ + static_cast<int>(rank) * (PJ / 2);
+      const int yx = tt * PT + half0, yw = jt * pj + static_cast<int>(rank) * (pj / 2);
       for (int kb = 0; kb < a.nkb; ++kb) {
         if (!mbar_wait_warp(&empty[s], ph)) { ok = false; break; }
         if (leader) {
           const uint32_t st = base + s * S::kStage;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kStage);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
           tma_load_2d_pair(st, &tmX, full0 + 8 * s, kb * PK, yx);
           tma_load_2d_pair(st + S::kX, &tmW, full0 + 8 * s, kb * PK, yw);
         }
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(PairShape<PJ, TMA>::kThreads, 1)
       const bool leader = elect_one();
       bool ok = true;
       uint32_t s = 0, ph = 0, ch = 0;
-      constexpr uint32_t idesc = idesc_s8_s32(PT, PJ);
+      const uint32_t idesc = idesc_s8_s32(PT, pj);
       const uint64_t dx0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
       const uint64_t dw0 = smem_desc_sw128(smem_u32(smem) + S::kX, 16, 1024);
       for (int t = pair; t < n_tiles && ok; t += n_pairs, ++ch) {
@@ -498,6 +501,7 @@ __global__ void __launch_bounds__(PairShape<PJ, TMA>::kThreads, 1)
   } else {
     constexpr int BC = 64 / sizeof(T);            // outputs per staged box
     const int ew = warp - 2, quarter = warp & 3, col0 = (ew >> 2) * S::kCols;
+    const int blocks = min(S::kCols, pj - col0) / 32;  // of 32 outputs that this warp has in a tile
     uint8_t *stg = staging + ew * S::kStaging;
     uint32_t stg_at = 0;
     Cols &cl = cols[ew];
@@ -505,7 +509,7 @@ __global__ void __launch_bounds__(PairShape<PJ, TMA>::kThreads, 1)
       TileOps o{};
       if (t >= n_tiles) return o;
       pair_tile(t, a.n_tt, a.n_jt, o.tt, o.jt);
-      const int64_t j0 = static_cast<int64_t>(o.jt) * PJ + col0 + lane;
+      const int64_t j0 = static_cast<int64_t>(o.jt) * pj + col0 + lane;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         if (j0 + 32 * i < a.d_out) {
@@ -546,11 +550,11 @@ __global__ void __launch_bounds__(PairShape<PJ, TMA>::kThreads, 1)
         if (a.r) r.load(a, a.r, row0, j, lane);
       };
       if (a.m || a.r) {
-        if (kEarly) load_mr(static_cast<int64_t>(jt) * PJ + col0);
+        if (kEarly) load_mr(static_cast<int64_t>(jt) * pj + col0);
         if (t + n_pairs < n_tiles) {
           const int64_t next_row = static_cast<int64_t>(next.tt) * PT + half0 + quarter * 32 + lane;
-          const int64_t jw = static_cast<int64_t>(next.jt) * PJ + col0;
-          for (int64_t j = jw; next_row < a.n_tok && j < jw + S::kCols && j < a.d_out; j += 128 / sizeof(T)) {
+          const int64_t jw = static_cast<int64_t>(next.jt) * pj + col0;
+          for (int64_t j = jw; next_row < a.n_tok && j < jw + blocks * 32 && j < a.d_out; j += 128 / sizeof(T)) {
             if (a.m) prefetch_l2(static_cast<const T *>(a.m) + next_row * a.d_out + j);
             if (a.r) prefetch_l2(static_cast<const T *>(a.r) + next_row * a.d_out + j);
           }
@@ -575,7 +579,7 @@ __global__ void __launch_bounds__(PairShape<PJ, TMA>::kThreads, 1)
         }
         constexpr int R = S::kRows;                                // rows that the buffer holds
         float *rows = reinterpret_cast<float *>(stg);
-        const int64_t j0 = static_cast<int64_t>(jt) * PJ + col0, left = a.n_tok - row0;
+        const int64_t j0 = static_cast<int64_t>(jt) * pj + col0, left = a.n_tok - row0;
         const int n = a.d_out - j0 < 64 ? static_cast<int>(a.d_out - j0) : 64;
 #pragma unroll 1
         for (int p = 0; p < 32; p += R) {
@@ -596,11 +600,11 @@ __global__ void __launch_bounds__(PairShape<PJ, TMA>::kThreads, 1)
       // (rolled: the options' code per 32 columns is large, and the warps
       // would wait for instructions)
 #pragma unroll 1
-      for (int q = 0; q < S::kCols / 32; ++q) {
-        const int64_t j0 = static_cast<int64_t>(jt) * PJ + col0 + q * 32;
+      for (int q = 0; q < blocks; ++q) {
+        const int64_t j0 = static_cast<int64_t>(jt) * pj + col0 + q * 32;
         float v[32];
         tmem_ld32(taddr + q * 32, v);
-        if (q == S::kCols / 32 - 1) {
+        if (q == blocks - 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(&acc_empty[buf], 0);
@@ -629,7 +633,7 @@ __global__ void __launch_bounds__(PairShape<PJ, TMA>::kThreads, 1)
             r.to_row(box, lane);
             r.template plus<H>(v);
           }
-          if (kEarly && q + 1 < S::kCols / 32) load_mr(j0 + 32);
+          if (kEarly && q + 1 < blocks) load_mr(j0 + 32);
           stage_row<H>(box, lane, v, T());
           if constexpr (TMA) {
             fence_proxy_async_smem();
@@ -1004,19 +1008,20 @@ constexpr CUtensorMapDataType tmap_type() {
 }
 
 template <typename T, int PJ, bool TMA>
-gq_status launch_pair_as(W8Args a, cudaStream_t st) {
+gq_status launch_pair_as(W8Args a, int pj, cudaStream_t st) {
   using S = PairShape<PJ, TMA>;
   static SmemOptIn opt;
   CUtensorMap tX, tW, tY{};
   gq_status s = make_tmap_2d(&tX, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.d_in, a.n_tok, a.d_in, PK, 128);
   if (s == GQ_OK)
-    s = make_tmap_2d(&tW, a.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.d_in, a.d_out, a.d_in, PK, PJ / 2);
+    s = make_tmap_2d(&tW, a.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.d_in, a.d_out, a.d_in, PK, pj / 2);
   if (s == GQ_OK && TMA)
     s = make_tmap_2d(&tY, a.y, tmap_type<T>(), sizeof(T), a.d_out, a.n_tok, a.d_out, 64 / sizeof(T),
                      32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (s != GQ_OK) return s;
   a.n_tt = static_cast<int>((a.n_tok + PT - 1) / PT);
-  a.n_jt = static_cast<int>((a.d_out + PJ - 1) / PJ);
+  a.n_jt = static_cast<int>((a.d_out + pj - 1) / pj);
+  a.pj = pj;
   a.nkb = (a.d_in + PK - 1) / PK;
   const int tiles = a.n_tt * a.n_jt, pairs = num_sms() / 2;
   opt.allow(w8a8_pair_kernel<T, PJ, TMA>, S::kSmem);
@@ -1034,11 +1039,11 @@ bool whole_rows(const W8Args &a) {
   return a.d_out * sizeof(T) % 16 == 0;
 }
 template <typename T, int PJ>
-gq_status launch_pair(const W8Args &a, cudaStream_t st) {
+gq_status launch_pair(const W8Args &a, int pj, cudaStream_t st) {
   if constexpr (sizeof(T) == 4 && PJ == 256)          // (ragged fp32 rows: 128 or few tiles)
-    return launch_pair_as<T, PJ, true>(a, st);
+    return launch_pair_as<T, PJ, true>(a, pj, st);
   else
-    return whole_rows<T>(a) ? launch_pair_as<T, PJ, true>(a, st) : launch_pair_as<T, PJ, false>(a, st);
+    return whole_rows<T>(a) ? launch_pair_as<T, PJ, true>(a, pj, st) : launch_pair_as<T, PJ, false>(a, pj, st);
 }
 
 // CTAs per tile: the split whose fullest SM has the fewest K steps, the
@@ -1136,18 +1141,32 @@ gq_status launch_vec(const W8Args &a, cudaStream_t st) {
 
 // Expected microseconds of a pair kernel: launch and first loads, the first
 // tile's MMAs, a round of tiles per 74 pairs, each bound by its MMAs or by its
-// epilogue, and the last epilogue.  Steps of 0.35 (PJ = 256) and 0.23 us (128):
-// an N = 128 MMA reads its A tile twice as often per flop.
+// epilogue, and the last epilogue.  Steps of 0.35 (256 outputs) and 0.23 us
+// (128): a narrow MMA reads its A tile more often per flop.  `pj`: the tile's
+// outputs; 224 instead of 256 where the last round is so poorly filled that as
+// many rounds of smaller tiles do (2560 x 2048 x 8192: 320 or 370 tiles, five
+// rounds either way, 35.2 or 33.6 us; each epilogue warp keeps 32 outputs or
+// more, so no less).
 template <typename T, int PJ>
-float pair_us(const W8Args &a, int nkb) {
-  const int64_t tiles = ((a.n_tok + PT - 1) / PT) * ((a.d_out + PJ - 1) / PJ), pairs = num_sms() / 2;
-  const float rounds = static_cast<float>((tiles + pairs - 1) / pairs);
+float pair_us(const W8Args &a, int nkb, int &pj) {
+  const int64_t n_tt = (a.n_tok + PT - 1) / PT, pairs = num_sms() / 2;
   const bool whole = whole_rows<T>(a), wide = PJ == 256;
   if (!whole && wide && sizeof(T) == 4) return FLT_MAX;
-  const float epi = sizeof(T) == 4 ? (whole ? (wide ? 4.7f : 3.2f) : 4.0f)
-                                   : (whole ? (wide ? 3.8f : 2.5f) : (wide ? 5.5f : 3.8f));
-  const float mma = static_cast<float>(nkb) * (wide ? 0.35f : 0.23f);
-  return 3.5f + mma + (rounds - 1.0f) * (mma > epi ? mma : epi) + epi;
+  const float epi_full = sizeof(T) == 4 ? (whole ? (wide ? 4.7f : 3.2f) : 4.0f)
+                                        : (whole ? (wide ? 3.8f : 2.5f) : (wide ? 5.5f : 3.8f));
+  float best = FLT_MAX;
+  for (int c = PJ; c >= (wide ? 224 : PJ); c -= 32) {
+    const int64_t tiles = n_tt * ((a.d_out + c - 1) / c);
+    const float rounds = static_cast<float>((tiles + pairs - 1) / pairs);
+    const float epi = epi_full * static_cast<float>(c) / PJ;
+    const float mma = static_cast<float>(nkb) * (0.11f + 0.24f / 256.0f * static_cast<float>(c));
+    const float us = 3.5f + mma + (rounds - 1.0f) * (mma > epi ? mma : epi) + epi;
+    if (us < best) {
+      best = us;
+      pj = c;
+    }
+  }
+  return best;
 }
 // Of the kernel for few tiles: launch and first loads, the weights from HBM or
 // the fullest SM's steps, and the epilogues (of tiles that share an SM they
@@ -1188,9 +1207,10 @@ gq_status launch_typed(W8Args a, cudaStream_t st) {
   f.nkb = (a.d_in + PK - 1) / PK;
   const FewPlan p = few_plan(a.n_tok, a.d_out, f.nkb, f.n_tt, f.n_jt);
   const float few = few_us(a, p);
-  const float wide = pair_us<T, 256>(a, f.nkb), narrow = pair_us<T, 128>(a, f.nkb);
+  int pj = 256, pj128 = 128;
+  const float wide = pair_us<T, 256>(a, f.nkb, pj), narrow = pair_us<T, 128>(a, f.nkb, pj128);
   if (few <= wide && few <= narrow) return launch_few<T>(f, p, st);
-  return wide <= narrow ? launch_pair<T, 256>(a, st) : launch_pair<T, 128>(a, st);
+  return wide <= narrow ? launch_pair<T, 256>(a, pj, st) : launch_pair<T, 128>(a, pj128, st);
 }
 
 }  // namespace
@@ -1205,7 +1225,7 @@ gq_status launch_w8a8(const int8_t *w_codes, const uint16_t *w_scales, const int
     return check_launch("memset");
   }
   const W8Args a{w_codes, x_codes, w_scales, w_zpoint, x_scales, x_sums, bias, M, R, Y,
-                 d_out,   n_tok,   static_cast<int>(d_in), act, status, 0, 0, 0};
+                 d_out,   n_tok,   static_cast<int>(d_in), act, status, 0, 0, 0, 0};
   switch (y_dtype) {
     case GQ_F32: return launch_typed<float>(a, st);
     case GQ_F16: return launch_typed<__half>(a, st);
