@@ -43,11 +43,18 @@ __device__ __forceinline__ int sub_wrap(int acc, int z, int xsum) {
 // (c0 + c1 v^2), two at a time.  The approximate 2^t and reciprocal (a few
 // ulps, and t's rounding) matter where 2^t is near 1; where it is large the
 // value itself vanishes.  NaN stays NaN, in ReLU too.
-__device__ __forceinline__ float over_1_plus_exp2(float v, float t) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  return v * r;
+__device__ __forceinline__ void over_1_plus_exp2(uint64_t v, uint64_t t, float &lo, float &hi) {
+  uint32_t t0, t1;
+  float e0, e1;
+  f32x2_unpack(t, t0, t1);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(__uint_as_float(t0)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(__uint_as_float(t1)));
+  f32x2_unpack(add2(f32x2_pack(e0, e1), f32x2_pack(1.0f, 1.0f)), t0, t1);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(__uint_as_float(t0)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(__uint_as_float(t1)));
+  f32x2_unpack(mul2(v, f32x2_pack(e0, e1)), t0, t1);
+  lo = __uint_as_float(t0);
+  hi = __uint_as_float(t1);
 }
 template <int N>
 __device__ __forceinline__ void act_all(float (&v)[N], int act) {
@@ -59,10 +66,8 @@ __device__ __forceinline__ void act_all(float (&v)[N], int act) {
     const uint64_t c = f32x2_pack(-1.4426950408889634f, -1.4426950408889634f);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      uint32_t t0, t1;
-      f32x2_unpack(mul2(f32x2_pack(v[i], v[i + 1]), c), t0, t1);
-      v[i] = over_1_plus_exp2(v[i], __uint_as_float(t0));
-      v[i + 1] = over_1_plus_exp2(v[i + 1], __uint_as_float(t1));
+      const uint64_t p = f32x2_pack(v[i], v[i + 1]);
+      over_1_plus_exp2(p, mul2(p, c), v[i], v[i + 1]);
     }
   } else if (act == GQ_ACT_GELU) {
     const uint64_t c0 = f32x2_pack(-2.302208198f, -2.302208198f);    // -2 log2(e) sqrt(2 / pi)
@@ -70,10 +75,7 @@ __device__ __forceinline__ void act_all(float (&v)[N], int act) {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
       const uint64_t p = f32x2_pack(v[i], v[i + 1]);
-      uint32_t t0, t1;
-      f32x2_unpack(mul2(p, fma2(mul2(p, p), c1, c0)), t0, t1);
-      v[i] = over_1_plus_exp2(v[i], __uint_as_float(t0));
-      v[i + 1] = over_1_plus_exp2(v[i + 1], __uint_as_float(t1));
+      over_1_plus_exp2(p, mul2(p, fma2(mul2(p, p), c1, c0)), v[i], v[i + 1]);
     }
   }
 }
@@ -109,8 +111,8 @@ __device__ __forceinline__ OutCol out_col(const W8Args &a, int64_t j, bool live)
 __device__ __forceinline__ float finish(const W8Args &a, const OutCol &o, int acc, float xs,
                                         int xsum, float m, float r) {
   if (a.wz) acc = sub_wrap(acc, o.wz, xsum);
-  float v[2] = {static_cast<float>(acc) * o.scale() * xs, 0.0f};
-  if (a.bias) v[0] += o.bias;
+  float v[2] = {static_cast<float>(acc) * o.scale(), 0.0f};
+  v[0] = a.bias ? fmaf(v[0], xs, o.bias) : v[0] * xs;
   act_all(v, a.act);
   if (a.m) v[0] *= m;
   if (a.r) v[0] += r;
@@ -142,16 +144,19 @@ __device__ __forceinline__ void scale32(const W8Args &a, const float *s, const i
 #pragma unroll
   for (int i = 0; i < 16; i += 2) {
     const ulonglong2 s4 = *reinterpret_cast<const ulonglong2 *>(s + 2 * i);
-    p[i] = mul2(mul2(int2float2(v[2 * i], v[2 * i + 1]), s4.x), xs2);
-    p[i + 1] = mul2(mul2(int2float2(v[2 * i + 2], v[2 * i + 3]), s4.y), xs2);
+    p[i] = mul2(int2float2(v[2 * i], v[2 * i + 1]), s4.x);
+    p[i + 1] = mul2(int2float2(v[2 * i + 2], v[2 * i + 3]), s4.y);
   }
   if (a.bias) {
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
       const ulonglong2 b4 = *reinterpret_cast<const ulonglong2 *>(b + 2 * i);
-      p[i] = add2(p[i], b4.x);
-      p[i + 1] = add2(p[i + 1], b4.y);
+      p[i] = fma2(p[i], xs2, b4.x);
+      p[i + 1] = fma2(p[i + 1], xs2, b4.y);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i] = mul2(p[i], xs2);
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -325,7 +330,7 @@ __device__ __forceinline__ void store_box(const W8Args &a, const uint8_t *stg, i
 //               by TMA store; where Y's rows are no multiple of 16 bytes
 //               (!TMA), by ordinary ones.  No warp waits for another one's tile
 //               (operands shared by a barrier of all: 2560 x 2048 x 8192 with
-//               GELU 42.7 us, so 40.5).
+//               GELU 42.7 us, so 40.5; 36.9 with all later steps).
 // The issuing warps' lanes walk their loops together, so that a step's values
 // stay in uniform registers (a loop of one lane: 0.35 us a step, so 0.25: they
 // share their schedulers with the epilogue).  Bound by the tensor cores where K
@@ -726,11 +731,10 @@ __device__ __forceinline__ void few_columns(const W8Args &a, const OutCol &o, bo
   float v[NC];
   const float ws = o.scale();
 #pragma unroll
-  for (int i = 0; i < NC; ++i)
-    v[i] = c0 + i * step < n ? static_cast<float>(acc[i]) * ws * xs[c0 + i * step] : 0.0f;
-  if (a.bias) {
-#pragma unroll
-    for (int i = 0; i < NC; ++i) v[i] += o.bias;
+  for (int i = 0; i < NC; ++i) {
+    const float sx = c0 + i * step < n ? xs[c0 + i * step] : 0.0f;
+    v[i] = static_cast<float>(acc[i]) * ws;
+    v[i] = a.bias ? fmaf(v[i], sx, o.bias) : v[i] * sx;
   }
   act_all(v, a.act);
   if (a.m) {
