@@ -281,6 +281,16 @@ def test_product_by_inputs(n, d):
     _product(n, d, 200 if d < 8192 else 136, "f32", affine=d % 32 == 16, res=True)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m", [4000, 4001, 4004])
+@pytest.mark.parametrize("n", [600, 1300])
+def test_product_in_many_tiles(n, m, dt):
+    """One and several rounds of tiles on all SMs, rows of whole 16 bytes and ragged ones."""
+    _product(n, 272, m, dt, affine=True, bias=True, act="gelu", mul=True, res=True)
+    if dt != "f16":
+        _product(n, 272, m, dt)
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
 @pytest.mark.parametrize("n", [1, 40, 400])
 def test_product_activations(n, act):
