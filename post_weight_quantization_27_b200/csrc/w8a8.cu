@@ -909,16 +909,17 @@ __global__ void __launch_bounds__(F_THREADS)
 }
 
 // ---------------------------------------------------------------- one to eight tokens
-// A warp reads V_R output rows 512 bytes at a time (16 per lane, two to four
-// steps in flight) straight from global memory and multiplies them with NT tokens by
-// dp4a; `ks` warps of a block share a row group along K and add up through
-// shared memory.  No barriers, no TMEM and no tensor maps to set up: the
+// A warp reads V_R = 4 or 8 output rows 512 bytes at a time (16 per lane, two
+// to four steps in flight) straight from global memory and multiplies them
+// with NT tokens by dp4a; `ks` warps of a block share a row group along K and
+// add up through shared memory.  No barriers, no TMEM and no tensor maps to set up: the
 // weights' bytes and one memory round trip are all there is.  HBM-bound: one
-// token 4096 -> 11008 9.8 us of 6.9 at the copy rate, 768 -> 2304 2.2 us.  The
+// token 4096 -> 11008 9.5 us of 6.9 at the copy rate, 8192 -> 28672 36.2 of
+// 35.9, 768 -> 2304 2.1 us.  The
 // first steps' weights start towards L2 before the stream's earlier work is
 // done (whose results they may be: nothing is read yet): behind a token's norm
 // 11.5 us instead of 12.3, 768 -> 2304 3.9 instead of 4.1.
-constexpr int V_R = 4, V_WARPS = 4;
+constexpr int V_WARPS = 4;
 
 __device__ __forceinline__ int4 ld_stream(const int8_t *p) {  // (not .nc: see chain_wait)
   int4 v;
@@ -929,13 +930,13 @@ __device__ __forceinline__ int4 ld_stream(const int8_t *p) {  // (not .nc: see c
   return v;
 }
 
-template <typename T, int NT>
+template <typename T, int NT, int V_R>
 __global__ void __launch_bounds__(V_WARPS * 32) w8a8_vec_kernel(W8Args a, int ks) {
   __shared__ int part[V_WARPS][V_R * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = V_WARPS / ks, kp = warp % ks, grp = warp / ks;
   const int64_t j0 = (static_cast<int64_t>(blockIdx.x) * groups + grp) * V_R;
-  constexpr int ST = NT == 1 ? 4 : 2;   // steps in flight
+  constexpr int ST = NT == 1 ? 16 / V_R : 2;   // steps in flight
   if (kp == 0 && lane < V_R && j0 + lane < a.d_out)
     prefetch_l2(a.w + (j0 + lane) * a.d_in, a.d_in < ST * ks * 512 ? a.d_in : ST * ks * 512);
   chain_wait();
@@ -1114,7 +1115,7 @@ gq_status launch_few(const W8Args &a, const FewPlan &p, cudaStream_t st) {
   return launched(e, "w8a8_few_kernel");
 }
 
-template <typename T, int NT>
+template <typename T, int NT, int V_R = 4>
 gq_status launch_vec_n(const W8Args &a, cudaStream_t st) {
   // warps along K: while the row groups alone do not fill the SMs
   int ks = 1;
@@ -1122,7 +1123,7 @@ gq_status launch_vec_n(const W8Args &a, cudaStream_t st) {
   while (ks < V_WARPS && rows * ks < 8 * static_cast<int64_t>(num_sms()) && a.d_in > 512 * ks) ks *= 2;
   const int64_t groups = V_WARPS / ks;
   const int slot = timer_begin(GQ_KERNEL_W8A8, st);
-  const cudaError_t e = launch_chained(w8a8_vec_kernel<T, NT>, static_cast<unsigned>((rows + groups - 1) / groups),
+  const cudaError_t e = launch_chained(w8a8_vec_kernel<T, NT, V_R>, static_cast<unsigned>((rows + groups - 1) / groups),
                                        V_WARPS * 32, 0, st, 1, a, ks);
   count_launch();
   timer_end(slot, st, 2.0 * static_cast<double>(a.n_tok) * a.d_out * a.d_in);
@@ -1132,7 +1133,9 @@ gq_status launch_vec_n(const W8Args &a, cudaStream_t st) {
 template <typename T>
 gq_status launch_vec(const W8Args &a, cudaStream_t st) {
   switch (a.n_tok) {
-    case 1: return launch_vec_n<T, 1>(a, st);
+    case 1:  // (short rows: 768 -> 50257 9.6 us by eights, 13.7 by fours)
+      return a.d_in <= 1024 && a.d_out >= int64_t(64) * num_sms() ? launch_vec_n<T, 1, 8>(a, st)
+                                                                  : launch_vec_n<T, 1>(a, st);
     case 2: return launch_vec_n<T, 2>(a, st);
     case 3: return launch_vec_n<T, 3>(a, st);
     case 4: return launch_vec_n<T, 4>(a, st);

@@ -281,6 +281,13 @@ def test_product_by_inputs(n, d):
     _product(n, d, 200 if d < 8192 else 136, "f32", affine=d % 32 == 16, res=True)
 
 
+@pytest.mark.parametrize("d", [16, 272, 768, 1024])
+def test_product_of_one_token_with_many_short_rows(d):
+    for m in (9472, 9479, 20001):
+        _product(1, d, m, "f32", affine=True, bias=True, act="silu", mul=True, res=True)
+    _product(1, d, 9473, "bf16")
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("m", [4000, 4001, 4004])
 @pytest.mark.parametrize("n", [600, 1300])
