@@ -461,9 +461,10 @@ __global__ void __launch_bounds__(N == 8 ? 1024 : 256, N == 8 ? 1 : 3) quant_blo
 // the next row's.  x (and r) are read, codes (and h) written: plain rows and
 // fp32 rows are bound by HBM (16384 x 28672 bf16 204 us = 105% of the copy
 // bandwidth, 16384 x 8192 fp32 with factors 104 us = 99%), 16-bit rows with
-// factors also by the instructions issued, about 16 an element with column
-// factors and 21 with the norm against 11 plain (16384 x 28672 263 us = 82%,
-// 32768 x 8192 norm with residual 306 us = 94%, without 216 us = 57%).
+// factors also by the instructions issued, 14 an element with column factors,
+// 21 with the norm and 27 with its residual against 12 plain (16384 x 28672
+// 263 us = 82%, 32768 x 8192 norm with residual 306 us = 94%, without 216 us
+// = 57%).
 constexpr int kRegThreads = 640;
 constexpr size_t kRingMost = 225 * 1024;
 __device__ __forceinline__ void cp_async16(uint32_t dst, const char *src) {
