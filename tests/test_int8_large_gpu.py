@@ -1,0 +1,143 @@
+"""int8 tokens and the norm in front of them at sizes of whole prompts: the persistent kernels over
+several rounds of rows, and a block per row of 32 elements per thread.  The reference is the definition in elementary torch operations on the GPU (codes
+in IEEE fp32, which defines them, the rest in 64 bits), the oracle on some of the rows."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from post_weight_quantization_27_b200 import gq
+from tests.test_int8_gpu import DT, U32
+
+pytestmark = pytest.mark.gpu
+
+
+def _gen(*seed):
+    return torch.Generator(device="cuda").manual_seed(sum(1009 ** i * s for i, s in enumerate(seed)))
+
+
+def _big(n, d, dt, seed, special=True):
+    """Tokens [n][d] with rows of zeros, NaN, an infinity, values whose squares overflow or vanish in
+    fp32 and subnormal ones among them, the last row of all included."""
+    g = _gen(n, d, seed)
+    x = torch.randn(n, d, generator=g, device="cuda")
+    x *= torch.exp(0.5 * torch.randn(d, generator=g, device="cuda"))
+    if special:
+        x[3] = 0
+        x[n // 2, d - 1] = float("nan")
+        x[n // 3, 0] = float("-inf")
+        x[n - 1, d // 2] = float("nan")
+        if dt != "f16":
+            x[5] *= 1e19
+            x[n - 2] *= 1e-25
+            x[n // 4] *= 1e-40
+    return x.to(DT[dt])
+
+
+def _rows_int8(g):
+    """Codes, steps and code sums of the rows of g (fp32, on the GPU)."""
+    bad = ~torch.isfinite(g).all(1)
+    g = torch.where(bad[:, None], torch.zeros_like(g), g)
+    top = g.abs().amax(1)
+    s = top / torch.full_like(top, 127.0)      # (by a tensor: by a number it is a product)
+    s = torch.where(s == 0, torch.ones_like(s), s)
+    c = (g / s[:, None]).round_().clamp_(-127, 127)
+    return (c.to(torch.int8), torch.where(bad, torch.full_like(s, float("nan")), s),
+            c.sum(1, dtype=torch.float64).to(torch.int32))
+
+
+def _same(a, b):
+    return bool(((a == b) | (torch.isnan(a) & torch.isnan(b))).all())
+
+
+def _some(n):
+    """Rows for the oracle: the special ones, the first and last few and some between."""
+    return sorted({*range(8), n // 4, n // 3, n // 2, *range(n - 5, n), *range(0, n, n // 11)})
+
+
+# Persistent blocks, two to 17 rounds of rows with a ragged last one, one to four rows a block, rows
+# that fill all threads' units and others, fp32 factors in registers (up to 20480 elements) and in
+# shared memory; then a block per row of 32 elements per thread, alone and in clusters.
+SIZES = [(301, 28672), (2051, 2064), (5001, 2048), (6001, 768), (80001, 48), (201, 20480),
+         (201, 20496), (9501, 1024), (512, 4096), (1501, 768), (301, 2064), (150, 16384),
+         (160, 40000)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("n,d", SIZES)
+def test_quantize_tokens(n, d, dt):
+    X = _big(n, d, dt, 1)
+    col = torch.exp(0.3 * torch.randn(d, generator=_gen(d), device="cuda"))
+    some = _some(n)
+    for cm, sums in ((None, True), (None, False), (col, True), (col, False)):
+        g = X.float() if cm is None else X.float() * cm
+        c, s, cs = _rows_int8(g)
+        q = gq.quantize_tokens_int8(X, cm, with_sums=sums)
+        assert torch.equal(q["codes"], c) and _same(q["scales"], s)
+        assert (q["sums"] is None) if not sums else torch.equal(q["sums"], cs)
+        oc, os_, osum = O.quantize_rows_int8(g[some].cpu().numpy())
+        assert np.array_equal(q["codes"][some].cpu().numpy(), oc)
+        assert np.array_equal(q["scales"][some].cpu().numpy(), os_, equal_nan=True)
+        assert not sums or np.array_equal(q["sums"][some].cpu().numpy(), osum)
+
+
+@pytest.mark.parametrize("n,d", [(301, 28672), (5001, 2048), (6001, 768), (512, 4096)])
+def test_quantize_rows_of_wider_ones_and_nothing_outside(n, d):
+    big = _big(n, d + 64, "bf16", 2, special=False)
+    before, X = big.clone(), big[:, 32:32 + d]
+    buf = torch.full((n + 4, d), 77, dtype=torch.int8, device="cuda")
+    sc = torch.full((n + 4,), 7.0, device="cuda")
+    sm = torch.full((n + 4,), 7, dtype=torch.int32, device="cuda")
+    gq.quantize_tokens_int8(X, out=dict(codes=buf[2:n + 2], scales=sc[2:n + 2], sums=sm[2:n + 2]))
+    c, s, cs = _rows_int8(X.float())
+    assert torch.equal(buf[2:n + 2], c) and torch.equal(sc[2:n + 2], s) and torch.equal(sm[2:n + 2], cs)
+    assert torch.equal(big, before)
+    for t, v in ((buf, 77), (sc, 7), (sm, 7)):
+        assert bool((t[:2] == v).all()) and bool((t[n + 2:] == v).all())
+
+
+def _check_norm(q, X, w, eps, R, sums):
+    d = X.shape[1]
+    h = X if R is None else (X.float() + R.float()).to(X.dtype)
+    if R is not None:
+        assert _same(q["h"].float(), h.float())
+    c, s, cs = _rows_int8(h.float() * w.float())
+    assert torch.equal(q["codes"], c)
+    assert (q["sums"] is None) if not sums else torch.equal(q["sums"], cs)
+    ref = s.double() / (h.double().square().mean(1) + float(np.float32(eps))).sqrt()
+    got = q["scales"].double()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    # The sum of squares: positive terms, each rounded and then added along a chain of at most d / 32
+    # + 64 additions, halved by the root; the division, the addition of eps, the root, the reciprocal,
+    # the step and its product: 6 half-steps more (of 2^-149 below the smallest normal number).
+    tol = ((d / 32 + 64) / 2 + 6) * U32
+    ok = ~torch.isnan(ref)
+    assert bool(((got - ref).abs()[ok] <= tol * ref[ok] + 2.0 ** -149).all())
+
+
+@pytest.mark.parametrize("dt,wdt", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f32", "f32")])
+@pytest.mark.parametrize("n,d", SIZES)
+def test_rmsnorm(n, d, dt, wdt):
+    X, R = _big(n, d, dt, 1), _big(n, d, dt, 3, special=False)
+    w = (1 + 0.2 * torch.randn(d, generator=_gen(d, 5), device="cuda")).to(DT[wdt])
+    for eps, sums in ((1e-5, True), (1e-30, False)):
+        _check_norm(gq.rmsnorm_quantize_int8(X, w, eps, R=R, with_sums=sums), X, w, eps, R, sums)
+        q = gq.rmsnorm_quantize_int8(X, w, eps, with_sums=sums)
+        _check_norm(q, X, w, eps, None, sums)
+    some = _some(n)
+    h, oc, os_, osum = O.rmsnorm_int8(X[some].float().cpu().numpy(), w.float().cpu().numpy(), 1e-30)
+    assert np.array_equal(q["codes"][some].cpu().numpy(), oc)
+
+
+@pytest.mark.parametrize("into", ["X", "R"])
+@pytest.mark.parametrize("n,d", [(301, 28672), (5001, 2048), (6001, 768), (512, 4096), (150, 16384)])
+def test_rmsnorm_in_place(n, d, into):
+    """h written over X or R while rows ahead are on their way; the squares of some rows overflow
+    fp32, so that they are added again from h."""
+    X, R = _big(n, d, "bf16", 1), _big(n, d, "bf16", 3, special=False)
+    w = torch.linspace(0.5, 1.5, d, device="cuda")
+    x, r = X.clone(), R.clone()
+    q = gq.rmsnorm_quantize_int8(x, w, R=r, H=x if into == "X" else r)
+    assert q["h"] is (x if into == "X" else r)
+    assert _same((r if into == "X" else x).float(), (R if into == "X" else X).float())
+    _check_norm(q, X, w, 1e-5, R, True)
