@@ -1,5 +1,6 @@
-"""int8 tokens and the norm in front of them at sizes of whole prompts: the persistent kernels over
-several rounds of rows, and a block per row of 32 elements per thread.  The reference is the definition in elementary torch operations on the GPU (codes
+"""int8 tokens, the norm in front of them and their product at sizes of whole prompts: the
+persistent kernels over several rounds of rows and tiles, and a block per row of 32 elements per
+thread.  The reference is the definition in elementary torch operations on the GPU (codes
 in IEEE fp32, which defines them, the rest in 64 bits), the oracle on some of the rows."""
 import numpy as np
 import pytest
@@ -7,7 +8,7 @@ import torch
 
 import oracle as O
 from post_weight_quantization_27_b200 import gq
-from tests.test_int8_gpu import DT, U32
+from tests.test_int8_gpu import DT, U32, _layer, _mlp_layers, _tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -141,3 +142,112 @@ def test_rmsnorm_in_place(n, d, into):
     assert q["h"] is (x if into == "X" else r)
     assert _same((r if into == "X" else x).float(), (R if into == "X" else X).float())
     _check_norm(q, X, w, 1e-5, R, True)
+
+
+# ------------------------------------------------------------------ the product
+
+def _act64(v, act):
+    if act == "gelu":
+        return 0.5 * v * (1.0 + torch.tanh((2.0 / np.pi) ** 0.5 * (v + 0.044715 * v ** 3)))
+    if act == "silu":
+        return v * torch.sigmoid(v)
+    return v.clamp(min=0.0) if act == "relu" else v
+
+
+def _product(n, d, m, dt, affine=False, bias=False, act="none", mul=False, res=False):
+    g = torch.Generator().manual_seed(7 * n + 3 * d + m)
+    (wc, ws, wz), (xc, xs, sums) = _layer(m, d, affine, g), _tokens(n, d, g)
+    wc, ws, xc, xs, sums = (t.cuda() for t in (wc, ws, xc, xs, sums))
+    wz = wz.cuda() if affine else None
+    gd = _gen(n, d, m)
+    b = torch.randn(m, generator=gd, device="cuda") if bias else None
+    M = torch.randn(n, m, generator=gd, device="cuda").to(DT[dt]) if mul else None
+    R = torch.randn(n, m, generator=gd, device="cuda").to(DT[dt]) if res else None
+    work = gq.workspace(gq.w8a8_workspace_size(m, d, n), "cuda")
+    Y = gq.w8a8_matmul(dict(codes=wc, scales=ws, zpoint=wz), dict(codes=xc, scales=xs, sums=sums),
+                       bias=b, act=act, mul=M, R=R, dtype=DT[dt], ws=work)
+    assert gq.workspace_status(work) == 0
+    # The integer sum (exact in fp64), two products and the bias round once each: 4 half-steps; the
+    # activation's slope is below 1.2, its own steps below 8 half-steps of its value and, where its
+    # exponent's rounding counts, 2^-20; M and R one half-step each, the output one of its type's.
+    wd = wc.double() - (0 if wz is None else wz.double()[:, None])
+    p = (xc.double() @ wd.t()) * ws.double().view(1, -1) * xs.double()[:, None]
+    base = p.abs()
+    if bias:
+        p, base = p + b.double(), base + b.double().abs()
+    v = _act64(p, act)
+    tol = 4 * U32 * base
+    if act in ("gelu", "silu"):
+        tol = 1.2 * tol + 8 * U32 * v.abs() + 2.0 ** -20 * base.clamp(max=1.0)
+    if mul:
+        v = v * M.double()
+        tol = tol * M.double().abs() + U32 * v.abs()
+    if res:
+        v = v + R.double()
+        tol = tol + U32 * v.abs()
+    step = torch.finfo(Y.dtype).eps / 2
+    tol = tol * (1 + step) + step * v.abs() + (2.0 ** -25 if dt == "f16" else 2.0 ** -140)
+    bad = (Y.double() - v).abs() > tol
+    assert not bool(bad.any()), (int(bad.sum()), bad.nonzero()[:4].tolist())
+
+
+ALL = dict(affine=True, bias=True, act="silu", mul=True, res=True)
+
+
+@pytest.mark.parametrize("n,d,m,dt", [
+    # 256 outputs a tile, 17 steps of K round the ring of five, two and three rounds of tiles (both
+    # accumulators used again), whole rows and ragged ones
+    (2048, 2064, 4608, "f16"), (3000, 2064, 4600, "bf16"), (3000, 2064, 4600, "f32"),
+    (3000, 2064, 4601, "bf16"), (2048, 2064, 4601, "f16"),
+    # 224 outputs a tile, three rounds
+    (2560, 2064, 4608, "bf16"),
+    # 128 outputs a tile, three to six rounds
+    (520, 2064, 8000, "f32"), (520, 2064, 8001, "bf16"), (3000, 2064, 4601, "f32")])
+def test_product_of_prompts(n, d, m, dt):
+    _product(n, d, m, dt, **ALL)
+    _product(n, d, m, dt, act="gelu", bias=True)
+    _product(n, d, m, dt)
+
+
+# ------------------------------------------------------------------ used together
+
+def test_calls_behind_one_another_see_each_others_results():
+    """A chain of dependent calls on a whole prompt (persistent rows, several tiles a pair), at once
+    and captured into a graph, gives what it gives with a synchronisation behind every call."""
+    n, d = 3000, 2048
+    w, _, _ = _mlp_layers(d, d)
+    nw = torch.linspace(0.5, 1.5, d, device="cuda")
+    x0, h0 = _big(n, d, "bf16", 1, special=False), _big(n, d, "bf16", 2, special=False)
+    x, h, y = x0.clone(), h0.clone(), torch.empty_like(x0)
+    tok = gq.quantize_tokens_int8(x)
+
+    def chain(sync=lambda: None):
+        x.copy_(x0)
+        h.copy_(h0)
+        for i in range(12):
+            q = gq.rmsnorm_quantize_int8(x, nw, R=h, H=h, out=tok)
+            sync()
+            gq.w8a8_matmul(w, q, act="silu", Y=y)
+            sync()
+            gq.quantize_tokens_int8(y, out=tok)
+            sync()
+            gq.w8a8_matmul(w, tok, R=y, Y=x)
+            sync()
+            if i % 4 == 3:
+                y.fill_(float("nan"))
+                h.mul_(0.5)
+    chain(torch.cuda.synchronize)
+    ref = x.clone(), h.clone()
+    assert bool(torch.isfinite(ref[0]).all()) and bool(torch.isfinite(ref[1]).all())
+    for _ in range(3):
+        chain()
+        assert torch.equal(x, ref[0]) and torch.equal(h, ref[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for _ in range(3):
+        x.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(x, ref[0]) and torch.equal(h, ref[1])
+    del graph
