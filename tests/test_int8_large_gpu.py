@@ -1,13 +1,14 @@
 """int8 tokens, the norm in front of them and their product at sizes of whole prompts: the
-persistent kernels over several rounds of rows and tiles, and a block per row of 32 elements per
-thread.  The reference is the definition in elementary torch operations on the GPU (codes
+persistent kernels over several rounds of rows and tiles, a block per row of 32 elements per thread,
+and GPTQ's layers.  The reference is the definition in elementary torch operations on the GPU (codes
 in IEEE fp32, which defines them, the rest in 64 bits), the oracle on some of the rows."""
 import numpy as np
 import pytest
 import torch
 
 import oracle as O
-from post_weight_quantization_27_b200 import gq
+from post_weight_quantization_27_b200 import gq, inputs as I
+from tests.gpu_util import u32
 from tests.test_int8_gpu import DT, U32, _layer, _mlp_layers, _tokens
 
 pytestmark = pytest.mark.gpu
@@ -251,3 +252,34 @@ def test_calls_behind_one_another_see_each_others_results():
         torch.cuda.synchronize()
         assert torch.equal(x, ref[0]) and torch.equal(h, ref[1])
     del graph
+
+
+# ------------------------------------------------------------------ layers of GPTQ
+
+@pytest.mark.parametrize("bits", [2, 3, 4, 8])
+@pytest.mark.parametrize("sym", [True, False])
+@pytest.mark.parametrize("group,order", [(-1, False), (-1, True), (0, False)])
+def test_layers_of_gptq(bits, sym, group, order):
+    """Layers that GPTQ writes, in the columns' own order and by falling diagonal: codes and
+    zero-points as packed, products those of the dequantised weights."""
+    d, m, n = 320, 150, 400
+    W, X = I.random_layer(40 + bits, d, m, n_tok=n)
+    Wd, Xd = W.float().cuda(), torch.as_tensor(X).to(torch.bfloat16).cuda()
+    U, perm, dead, _ = gq.damp_cholesky_inverse(gq.hessian(Xd), 0.01, act_order=order)
+    q = gq.gptq_quantize_layer(Wd, U, bits, group, 128, sym, perm=perm, dead=dead)
+    w = gq.unpack_int8(q, d, group, sym)
+    off = 1 << (bits - 1)
+    codes = O.unpack_nibbles(u32(q["qpacked"]), d, sym, bits=bits).astype(np.int64) - (0 if sym else off)
+    assert np.array_equal(w["codes"].cpu().numpy(), codes)
+    if not sym:
+        assert np.array_equal(w["zpoint"].cpu().numpy(), q["zeros"].cpu().numpy()[:, 0].astype(np.int64) - off)
+    W_hat = O.dequantize_packed(u32(q["qpacked"]), q["scales"].cpu().numpy(),
+                                None if sym else q["zeros"].cpu().numpy(), d, group, sym,
+                                None if q["g_idx"] is None else q["g_idx"].cpu().numpy(), bits)
+    for k in (1, 5, 60, n):
+        x = gq.quantize_tokens_int8(Xd[:k])
+        Y = gq.w8a8_matmul(w, x, dtype=torch.float32)
+        Xq = x["codes"].cpu().numpy() * x["scales"].cpu().numpy().astype(np.float64)[:, None]
+        want = Xq @ np.asarray(W_hat, dtype=np.float64).T
+        # the integer, two products and the output: 4 half-steps of fp32
+        assert np.all(np.abs(Y.double().cpu().numpy() - want) <= 4 * U32 * np.abs(want) + 1e-30)
