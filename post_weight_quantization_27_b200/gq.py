@@ -181,9 +181,23 @@ def _dev(t: torch.Tensor, name: str, dtype=None, shape=None) -> torch.Tensor:
     return t
 
 
-def workspace(nbytes: int, device) -> torch.Tensor:
-    """A caller-owned workspace buffer (256-byte aligned by the allocator)."""
-    return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
+def _new(shape, dtype, device, stream=None) -> torch.Tensor:
+    """A tensor that a call on ``stream`` (None: the current one) writes.  It comes from that
+    stream's own pool: a block of the current stream's could still be in use by work queued there
+    before it was freed, and could go to that stream again while the call runs.  The current stream,
+    which may read the tensor later, is made known to the allocator."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def workspace(nbytes: int, device, stream=None) -> torch.Tensor:
+    """A caller-owned workspace buffer (256-byte aligned by the allocator) for calls on ``stream``
+    (None: the current one)."""
+    return _new(max(int(nbytes), 1), torch.uint8, device, stream)
 
 
 def launch_count() -> int:
@@ -204,7 +218,7 @@ def selftest_bounded_wait(arrive: bool, limit_ns: int, stream=None) -> int:
     """Runs the bounded-wait self test and returns its status code (0, or 7
     when the wait gave up) without raising."""
     dev = torch.device("cuda", torch.cuda.current_device())
-    ws = workspace(256, dev)
+    ws = workspace(256, dev, stream)
     return int(lib().gq_selftest_bounded_wait(int(bool(arrive)), int(limit_ns), _p(ws),
                                               ws.numel(), _stream(stream)))
 
@@ -222,7 +236,7 @@ def hessian_accumulate(X: torch.Tensor, H: torch.Tensor, ws: torch.Tensor | None
     n_tok, d_in = X.shape
     _dev(H, "H", torch.float32, (d_in, d_in))
     need = hessian_workspace_size(n_tok, d_in)
-    ws = workspace(need, X.device) if ws is None else ws
+    ws = workspace(need, X.device, stream) if ws is None else ws
     _check(lib().gq_hessian_accumulate(_p(X), n_tok, d_in, _p(H), _p(ws), ws.numel(),
                                        _stream(stream)), "gq_hessian_accumulate")
     return H
@@ -234,9 +248,9 @@ def hessian(X: torch.Tensor, H: torch.Tensor | None = None, ws: torch.Tensor | N
     _dev(X, "X", torch.bfloat16)
     n_tok, d_in = X.shape
     if H is None:
-        H = torch.empty((d_in, d_in), dtype=torch.float32, device=X.device)
+        H = _new((d_in, d_in), torch.float32, X.device, stream)
     _dev(H, "H", torch.float32, (d_in, d_in))
-    ws = workspace(hessian_workspace_size(n_tok, d_in), X.device) if ws is None else ws
+    ws = workspace(hessian_workspace_size(n_tok, d_in), X.device, stream) if ws is None else ws
     _check(lib().gq_hessian_compute(_p(X), n_tok, d_in, _p(H), _p(ws), ws.numel(),
                                     _stream(stream)), "gq_hessian_compute")
     return H
@@ -259,12 +273,12 @@ def damp_cholesky_inverse(H: torch.Tensor, damp_percent: float = 0.01, act_order
     _dev(H, "H", torch.float32)
     d = H.shape[0]
     dev = H.device
-    U = torch.empty((d, d), dtype=torch.float32, device=dev) if U is None else _dev(U, "U", torch.float32, (d, d))
-    perm = torch.empty(d, dtype=torch.int32, device=dev) if act_order else None
-    dead = torch.empty(d, dtype=torch.uint8, device=dev)
-    info = torch.empty(1, dtype=torch.int32, device=dev)
+    U = _new((d, d), torch.float32, dev, stream) if U is None else _dev(U, "U", torch.float32, (d, d))
+    perm = _new(d, torch.int32, dev, stream) if act_order else None
+    dead = _new(d, torch.uint8, dev, stream)
+    info = _new(1, torch.int32, dev, stream)
     info_host = ctypes.c_int32(-1)
-    ws = workspace(damp_cholesky_workspace_size(d), dev) if ws is None else ws
+    ws = workspace(damp_cholesky_workspace_size(d), dev, stream) if ws is None else ws
     st = lib().gq_damp_cholesky_inverse(_p(H), d, float(damp_percent), int(bool(act_order)),
                                         _p(perm), _p(dead), _p(U), _p(info),
                                         ctypes.byref(info_host) if check else None,
@@ -282,10 +296,10 @@ def damp_cholesky_inverse_noalloc(H: torch.Tensor, damp_percent: float = 0.01,
     _dev(H, "H", torch.float32)
     d = H.shape[0]
     dev = H.device
-    U = torch.empty((d, d), dtype=torch.float32, device=dev) if U is None else _dev(U, "U", torch.float32, (d, d))
-    perm = torch.empty(d, dtype=torch.int32, device=dev) if act_order else None
-    dead = torch.empty(d, dtype=torch.uint8, device=dev)
-    info = torch.empty(1, dtype=torch.int32, device=dev)
+    U = _new((d, d), torch.float32, dev, stream) if U is None else _dev(U, "U", torch.float32, (d, d))
+    perm = _new(d, torch.int32, dev, stream) if act_order else None
+    dead = _new(d, torch.uint8, dev, stream)
+    info = _new(1, torch.int32, dev, stream)
     info_host = ctypes.c_int32(-1)
     st = lib().gq_damp_cholesky_inverse_noalloc(_p(H), d, float(damp_percent),
                                                 int(bool(act_order)), _p(perm), _p(dead), _p(U),
@@ -305,14 +319,14 @@ def _n_groups(d_in: int, group_size: int) -> int:
     return 1 if group_size <= 0 else d_in // group_size
 
 
-def _outputs(d_out, d_in, group_size, sym, dev, with_g_idx, bits=4):
+def _outputs(d_out, d_in, group_size, sym, dev, with_g_idx, bits=4, stream=None):
     """Output tensors of a quantised layer; the dict also records its code
     width (``bits``), which the consumers of the packed format read."""
     ng = _n_groups(d_in, group_size)
-    return dict(qpacked=torch.empty((d_out, bits * d_in // 32), dtype=torch.int32, device=dev),
-                scales=torch.empty((d_out, ng), dtype=torch.float16, device=dev),
-                zeros=None if sym else torch.empty((d_out, ng), dtype=torch.float16, device=dev),
-                g_idx=torch.empty(d_in, dtype=torch.int32, device=dev) if with_g_idx else None,
+    return dict(qpacked=_new((d_out, bits * d_in // 32), torch.int32, dev, stream),
+                scales=_new((d_out, ng), torch.float16, dev, stream),
+                zeros=None if sym else _new((d_out, ng), torch.float16, dev, stream),
+                g_idx=_new(d_in, torch.int32, dev, stream) if with_g_idx else None,
                 bits=bits)
 
 
@@ -331,9 +345,9 @@ def gptq_quantize_layer(W: torch.Tensor, U: torch.Tensor, bits: int = 4, group_s
         _dev(perm, "perm", torch.int32, (d_in,))
     if dead is not None:
         _dev(dead, "dead", torch.uint8, (d_in,))
-    o = _outputs(d_out, d_in, group_size, sym, W.device, perm is not None, bits) \
+    o = _outputs(d_out, d_in, group_size, sym, W.device, perm is not None, bits, stream) \
         if out is None else out
-    ws = workspace(gptq_workspace_size(d_out, d_in, block_size), W.device) if ws is None else ws
+    ws = workspace(gptq_workspace_size(d_out, d_in, block_size), W.device, stream) if ws is None else ws
     st = lib().gq_gptq_quantize_layer(_p(W), _DTYPES[W.dtype], d_out, d_in, _p(U), bits,
                                       group_size, block_size, int(bool(sym)), _p(perm), _p(dead),
                                       _p(o["qpacked"]), _p(o["scales"]), _p(o["zeros"]),
@@ -351,7 +365,8 @@ def rtn_quantize_pack(W: torch.Tensor, bits: int = 4, group_size: int = -1, sym:
     if W.dtype not in _DTYPES:
         raise ValueError(f"unsupported W dtype {W.dtype}")
     d_out, d_in = W.shape
-    o = _outputs(d_out, d_in, group_size, sym, W.device, False, bits) if out is None else out
+    o = _outputs(d_out, d_in, group_size, sym, W.device, False, bits, stream) \
+        if out is None else out
     st = lib().gq_rtn_quantize_pack(_p(W), _DTYPES[W.dtype], d_out, d_in, bits, group_size,
                                     int(bool(sym)), _p(o["qpacked"]), _p(o["scales"]),
                                     _p(o["zeros"]), _stream(stream))
@@ -375,8 +390,8 @@ def recon_error(W: torch.Tensor, q: dict, X: torch.Tensor, group_size: int = -1,
     _dev(X, "X", torch.bfloat16)
     d_out, d_in = W.shape
     n_tok = X.shape[0]
-    sse = torch.empty(1, dtype=torch.float64, device=W.device) if sse is None else sse
-    ws = workspace(recon_workspace_size(d_out, d_in, n_tok), W.device) if ws is None else ws
+    sse = _new(1, torch.float64, W.device, stream) if sse is None else sse
+    ws = workspace(recon_workspace_size(d_out, d_in, n_tok), W.device, stream) if ws is None else ws
     sse_h, mse_h = ctypes.c_double(0.0), ctypes.c_double(0.0)
     st = lib().gq_recon_error(_p(W), _DTYPES[W.dtype], _p(q["qpacked"]), _p(q["scales"]),
                               _p(q.get("zeros")), _p(q.get("g_idx")), d_out, d_in,
@@ -403,8 +418,8 @@ def recon_error_hessian(W: torch.Tensor, q: dict, H0: torch.Tensor, n_tok: int,
     _dev(W, "W")
     d_out, d_in = W.shape
     _dev(H0, "H0", torch.float32, (d_in, d_in))
-    sse = torch.empty(1, dtype=torch.float64, device=W.device) if sse is None else sse
-    ws = workspace(recon_error_hessian_workspace_size(d_out, d_in), W.device) if ws is None else ws
+    sse = _new(1, torch.float64, W.device, stream) if sse is None else sse
+    ws = workspace(recon_error_hessian_workspace_size(d_out, d_in), W.device, stream) if ws is None else ws
     sse_h, mse_h = ctypes.c_double(0.0), ctypes.c_double(0.0)
     st = lib().gq_recon_error_hessian(_p(W), _DTYPES[W.dtype], _p(q["qpacked"]),
                                       _p(q["scales"]), _p(q.get("zeros")), _p(q.get("g_idx")),
@@ -434,8 +449,8 @@ def w4a16_matmul(q: dict, d_in: int, X: torch.Tensor, group_size: int = -1, sym:
     _dev(X, "X", torch.bfloat16)
     d_out = q["qpacked"].shape[0]
     n_tok = X.shape[0]
-    Y = torch.empty((d_out, n_tok), dtype=torch.float32, device=X.device) if Y is None else Y
-    ws = workspace(w4a16_workspace_size(d_out, d_in, n_tok), X.device) if ws is None else ws
+    Y = _new((d_out, n_tok), torch.float32, X.device, stream) if Y is None else Y
+    ws = workspace(w4a16_workspace_size(d_out, d_in, n_tok), X.device, stream) if ws is None else ws
     st = lib().gq_w4a16_matmul(_p(q["qpacked"]), _p(q["scales"]), _p(q.get("zeros")),
                                _p(q.get("g_idx")), d_out, d_in, int(q.get("bits", 4)),
                                group_size, int(bool(sym)), _p(X), n_tok, _p(Y), _p(ws),
@@ -452,10 +467,10 @@ def qlinear_bf16(X: torch.Tensor, d_out: int, q: dict | None = None, W: torch.Te
     input, from the packed layer ``q`` or (q None) from dense weights W."""
     _dev(X, "X", torch.bfloat16)
     n_tok, d_in = X.shape
-    Z = torch.empty((n_tok, d_out), dtype=torch.bfloat16, device=X.device) if Z is None else Z
+    Z = _new((n_tok, d_out), torch.bfloat16, X.device, stream) if Z is None else Z
     if R is not None:
         _dev(R, "R", torch.bfloat16, (n_tok, d_out))
-    ws = workspace(256, X.device) if ws is None else ws
+    ws = workspace(256, X.device, stream) if ws is None else ws
     qq = q or {}
     st = lib().gq_qlinear_bf16(_p(qq.get("qpacked")), _p(qq.get("scales")), _p(qq.get("zeros")),
                                _p(qq.get("g_idx")), _p(W), _DTYPES.get(W.dtype, 0) if W is not None else 0,
@@ -481,22 +496,13 @@ def _arg(t: torch.Tensor, name: str, dtype, shape, dev: int) -> int:
     return t.data_ptr()
 
 
-def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
-    """A tensor that a call on ``stream`` writes: where that is not the current stream, the allocator
-    is told, so that the memory is not handed out again before that stream's work is done."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 def _tokens8(X: torch.Tensor, n_tok: int, d_in: int, with_sums: bool, out, stream, dev: int):
     """The dict of n_tok tokens to be written (that of ``out``, checked, or new tensors) and the
     addresses of its codes, scales and sums."""
     if out is None:
-        codes = _new((n_tok, d_in), torch.int8, X, stream)
-        scales = _new((n_tok,), torch.float32, X, stream)
-        sums = _new((n_tok,), torch.int32, X, stream) if with_sums else None
+        codes = _new((n_tok, d_in), torch.int8, X.device, stream)
+        scales = _new((n_tok,), torch.float32, X.device, stream)
+        sums = _new((n_tok,), torch.int32, X.device, stream) if with_sums else None
         return (dict(codes=codes, scales=scales, sums=sums), codes.data_ptr(), scales.data_ptr(),
                 _p(sums))
     codes, scales, sums = out["codes"], out["scales"], out.get("sums")
@@ -557,7 +563,7 @@ def rmsnorm_quantize_int8(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e
     if R is not None:
         pr = _arg(R, "R", xdt, shape, dev)
         if H is None:
-            H = _new(shape, xdt, X, stream)
+            H = _new(shape, xdt, X.device, stream)
         ph = _arg(H, "H", xdt, shape, dev)
     elif H is not None:
         raise ValueError("H is written only with a residual R")
@@ -583,8 +589,8 @@ def unpack_int8(q: dict, d_in: int, group_size: int = -1, sym: bool = True, stre
     _arg(q["scales"], "scales", torch.float16, (d_out, 1), dev)
     if not sym:
         _arg(q["zeros"], "zeros", torch.float16, (d_out, 1), dev)
-    codes = _new((d_out, d_in), torch.int8, qp, stream)
-    zp = None if sym else _new((d_out,), torch.int32, qp, stream)
+    codes = _new((d_out, d_in), torch.int8, qp.device, stream)
+    zp = None if sym else _new((d_out,), torch.int32, qp.device, stream)
     st = lib().gq_unpack_int8(_p(qp), None if sym else _p(q["zeros"]), d_out, d_in, bits,
                               int(bool(sym)), _p(codes), _p(zp), _stream(stream))
     _check(st, "gq_unpack_int8")
@@ -627,13 +633,13 @@ def w8a8_matmul(w: dict, x: dict, bias: torch.Tensor | None = None, act: str = "
     if Y is None:
         if dtype not in _DTYPES:
             raise ValueError(f"unsupported Y dtype {dtype}")
-        Y = _new(shape, dtype, xc, stream)
+        Y = _new(shape, dtype, xc.device, stream)
     ydt = Y.dtype
     dt = _DTYPES.get(ydt)
     if dt is None:
         raise ValueError(f"unsupported Y dtype {ydt}")
     if ws is None:
-        ws = _new((256,), torch.uint8, xc, stream)
+        ws = _new((256,), torch.uint8, xc.device, stream)
     elif ws.get_device() != dev:
         raise ValueError(f"ws is on {ws.device}, the current device is cuda:{dev}")
     st = lib().gq_w8a8_matmul(
@@ -668,7 +674,7 @@ def gptq_sequential(X0: torch.Tensor, layers: list, bits: int = 4, group_size: i
     for i, L in enumerate(layers):
         W = _dev(L["W"], "W")
         d_out, d_in = W.shape
-        o = _outputs(d_out, d_in, group_size, sym, dev, False, bits)
+        o = _outputs(d_out, d_in, group_size, sym, dev, False, bits, stream)
         outs.append(o)
         r = L.get("residual_from")
         arr[i] = SeqLayer(W.data_ptr(), _DTYPES[W.dtype], d_out, d_in, ACT[L.get("act", "none")],
@@ -677,10 +683,10 @@ def gptq_sequential(X0: torch.Tensor, layers: list, bits: int = 4, group_size: i
     lib_ = lib()
     need = int(lib_.gq_gptq_sequential_workspace_size(ctypes.addressof(arr), len(layers), n_tok,
                                                       block_size))
-    ws = workspace(need, dev)
-    sse = torch.empty(len(layers), dtype=torch.float64, device=dev)
+    ws = workspace(need, dev, stream)
+    sse = _new(len(layers), torch.float64, dev, stream)
     widths = [L["W"].shape[1] for L in layers] + [layers[-1]["W"].shape[0]]
-    X_all = torch.empty(n_tok * sum(widths), dtype=torch.bfloat16, device=dev)
+    X_all = _new(n_tok * sum(widths), torch.bfloat16, dev, stream)
     st = lib_.gq_gptq_sequential(_p(X0), n_tok, ctypes.addressof(arr), len(layers), bits,
                                  group_size, block_size, int(bool(sym)), float(damp_percent),
                                  _p(sse), _p(X_all), _p(ws), ws.numel(), _stream(stream))
@@ -712,11 +718,11 @@ def awq_rtn_search(W: torch.Tensor, H: torch.Tensor, X: torch.Tensor, bits: int 
     _dev(X, "X", torch.bfloat16)
     d_out, d_in = W.shape
     n_tok = X.shape[0]
-    o = _outputs(d_out, d_in, group_size, sym, W.device, False, bits)
-    col = torch.empty(d_in, dtype=torch.float32, device=W.device)
+    o = _outputs(d_out, d_in, group_size, sym, W.device, False, bits, stream)
+    col = _new(d_in, torch.float32, W.device, stream)
     mse = np.zeros(n_grid, dtype=np.float64)
     best = ctypes.c_int32(-1)
-    ws = workspace(awq_workspace_size(d_out, d_in, n_tok, group_size, sym, bits), W.device) \
+    ws = workspace(awq_workspace_size(d_out, d_in, n_tok, group_size, sym, bits), W.device, stream) \
         if ws is None else ws
     st = lib().gq_awq_rtn_search(_p(W), _DTYPES[W.dtype], d_out, d_in, _p(H), _p(X), n_tok, bits,
                                  group_size, int(bool(sym)), n_grid, _p(o["qpacked"]),
