@@ -695,7 +695,9 @@ def gptq_sequential(X0: torch.Tensor, layers: list, bits: int = 4, group_size: i
     for d in widths:
         xs.append(X_all[off:off + n_tok * d].view(n_tok, d))
         off += n_tok * d
-    return outs, sse.cpu().numpy().astype(np.float64), xs
+    with torch.cuda.stream(stream):      # (the copy waits for the call's stream)
+        errors = sse.cpu().numpy().astype(np.float64)
+    return outs, errors, xs
 
 
 # ------------------------------------------------------------------ activation-aware scaling

@@ -36,6 +36,7 @@ CALLS = {
     "rmsnorm_quantize_int8": lambda i, **s: gq.rmsnorm_quantize_int8(i["X"], i["nw"], R=i["X"], **s),
     "unpack_int8": lambda i, **s: gq.unpack_int8(i["q8"], D, **s),
     "w8a8_matmul": lambda i, **s: gq.w8a8_matmul(i["w8"], i["x8"], **s),
+    "gptq_sequential": lambda i, **s: gq.gptq_sequential(i["X"], [dict(W=i["W"], act="gelu")], 4, 64, **s),
     "awq_rtn_search": lambda i, **s: gq.awq_rtn_search(i["W"], i["H"], i["X"], 4, 64, n_grid=4, **s),
 }
 
