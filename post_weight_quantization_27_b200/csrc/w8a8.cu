@@ -1188,23 +1188,36 @@ float few_us(const W8Args &a, const FewPlan &p) {
 
 // The kernel is chosen by these estimates; dp4a for one token, and for up to
 // eight while the layer is small and its products few.  Measured (us, graph
-// replays, weights from HBM, bf16 out; fp32 in the last two lines):
-//   n    d_in   d_out    dp4a   few   256   128
-//   1    4096   11008     9.6  11.8  23.6  24.4
-//   1    28672  8192     36.6  40.9  82.2  88.7
-//   2    8192   8192     17.8  16.5  27.8  29.2
-//   4    4096   11008    11.3  11.8  22.1  22.3
-//   8    4096   4096      5.9   8.5  15.6  12.8
-//   8    4096   11008    14.8  11.9  21.0  20.9
-//   33   8192   28672       -  44.9  54.5  58.1
-//   64   8192   8192        -  19.8  27.3  20.1
-//   256  8192   8192        -  24.2  27.9  20.9
-//   384  4096   11008       -  22.3  27.7  24.7
-//   512  8192   8192        -  34.1  28.6  31.1
-//   512  4096   11008       -  29.9  28.3  25.2
-//   2048 4096   11008       - 100.4  62.8  69.2
-//   251  768    50257       -  28.3     -  29.8
-//   2048 2048   8191        -  51.5     -  38.7
+// replays, weights from HBM, bf16 out; fp32 in the last two lines; the chosen
+// one is marked):
+//   n    d_in   d_out    dp4a   few    256    128
+//   1    4096   11008     9.9*  11.8   24.3   25.8
+//   1    28672  8192     36.6*  41.2   82.7   86.0
+//   2    8192   8192     18.0   16.7*  30.6   31.1
+//   4    4096   4096      6.4*   8.6   14.6   12.6
+//   8    4096   4096      9.3*   8.6   14.8   12.9
+//   8    2048   8192      9.6*   8.0   11.6   10.7
+//   8    8192   2048      9.2*  15.6   22.4   16.2
+//   4    12288  2048      8.2*  18.2   30.5   22.8
+//   7    5120   5120     14.3*  10.7   17.5   19.5
+//   2    768    50257    11.2*   9.7   20.3   26.6
+//   5    768    50257    17.8*   9.8   20.3   26.0
+//   4    4096   11008    11.3*  12.0   21.9   23.4
+//   8    4096   11008    17.1   12.1*  21.0   21.9
+//   33   8192   28672       -   44.6*  52.3   58.8
+//   64   8192   8192        -   18.9*  26.6   20.2
+//   256  8192   8192        -   25.1   27.6   21.7*
+//   384  4096   11008       -   22.6*  26.2   24.8
+//   512  8192   8192        -   34.7   28.1*  31.4
+//   512  4096   11008       -   30.4   26.9*  25.5
+//   2048 4096   11008       -  102.5   61.7*  67.8
+//   251  768    50257       -   28.9*     -   30.0
+//   2048 2048   8191        -   51.3      -   38.8*
+// The bounds of dp4a are coarse: from two tokens on its time follows the
+// outputs as much as the layer's bytes, and the few-tile kernel's whether its
+// clusters run at once (16 to 18 tiles in eights or sevens seem not to), so
+// the slower one is taken for some layers, short rows with many outputs above
+// all (7 tokens 512 -> 32768: 13.2 us of 6.0).
 template <typename T>
 gq_status launch_typed(W8Args a, cudaStream_t st) {
   const int64_t layer = a.d_in * a.d_out;
