@@ -1089,7 +1089,8 @@ FewPlan few_plan(int64_t n_tok, int64_t d_out, int nkb, int &n_tt, int &n_jt) {
   if (p.stages > F_MAX_STAGES) p.stages = F_MAX_STAGES;
   const int most = (nkb + p.split - 1) / p.split;
   // a split tile's sums lie in the ring, which is at least 72 KB then
-  const int need = p.split > 1 ? ((p.bn > 128 ? p.bn * 512 : 72 * 1024) + stage - 1) / stage : 1;
+  static_assert(F_T * F_J * 4 <= 72 * 1024, "the sums of a tile fit the ring");
+  const int need = p.split > 1 ? (72 * 1024 + stage - 1) / stage : 1;
   if (p.stages > most) p.stages = most;
   if (p.stages < need) p.stages = need;
   p.tmem_cols = 32;
