@@ -33,7 +33,10 @@
  *     info_host, the reconstruction error with sse_host or mse_host, the
  *     scaling search) read that word and return GQ_ERR_TIMEOUT; an
  *     asynchronous caller reads it with gq_workspace_status() after the
- *     work, before reusing the workspace.  The Hessian and reconstruction
+ *     work, before reusing the workspace (calls that run at the same time
+ *     and share one, where it holds the status word only, leave each
+ *     other's results alone, but each clears the word as it starts, the
+ *     other's failure with it).  The Hessian and reconstruction
  *     error write NaN into their result when a wait gave up.
  *   - Shapes: W is d_out x d_in; X (calibration activations) is
  *     n_tok x d_in in bf16.  d_in must be a positive multiple of 8;
@@ -443,7 +446,8 @@ gq_status gq_rmsnorm_quantize_int8(const void *X, const void *R, gq_dtype x_dtyp
  *              may be Y itself
  *   Y          [n_tok][d_out] in y_dtype (device, out, 16-byte aligned)
  *   ws         >= gq_w8a8_workspace_size(d_out, d_in, n_tok) bytes (the
- *              device status word only)
+ *              device status word only); one for each call that may run
+ *              beside another and whose status is to be read
  * ---------------------------------------------------------------------- */
 enum { GQ_ACT_SILU = 3 };  /* gq_w8a8_matmul only */
 gq_status gq_unpack_int8(const uint32_t *qpacked, const uint16_t *zeros, int64_t d_out,

@@ -608,7 +608,8 @@ def w8a8_matmul(w: dict, x: dict, bias: torch.Tensor | None = None, act: str = "
     """Y [n_tok][d_out] = act(x W^T + bias) * mul + R from int8 tokens ``x`` (dict of
     quantize_tokens_int8 or rmsnorm_quantize_int8) and an int8 layer ``w`` (dict of unpack_int8).
     bias is fp32 [d_out]; mul and R have Y's shape and dtype (``dtype`` when Y is not given) and may
-    be Y itself; act is "none", "relu", "gelu" or "silu"."""
+    be Y itself; act is "none", "relu", "gelu" or "silu".  ``ws`` holds the status word, which each
+    call clears as it starts: calls at the same time need one each for workspace_status to tell."""
     wc, xc = w["codes"], x["codes"]
     n_tok, d_in = xc.shape
     d_out = wc.shape[0]
