@@ -439,8 +439,12 @@ gq_status gq_rmsnorm_quantize_int8(const void *X, const void *R, gq_dtype x_dtyp
  *   x_codes    [n_tok][d_in] int8 (device, 16-byte aligned); x_scales [n_tok]
  *              fp32; x_sums [n_tok] int32, read only with w_zpoint
  *   bias       [d_out] fp32 or NULL
- *   act        GQ_ACT_NONE, GQ_ACT_RELU, GQ_ACT_GELU or GQ_ACT_SILU
- *              (v / (1 + e^-v)); NaN stays NaN
+ *   act        GQ_ACT_NONE, GQ_ACT_RELU, GQ_ACT_GELU (tanh form) or
+ *              GQ_ACT_SILU (v / (1 + e^-v)); NaN stays NaN.  GELU and SiLU
+ *              use the hardware's approximate exponential and reciprocal, for
+ *              fp32 Y too: within 2^-21 of the value or 2^-20 absolutely (the
+ *              relative error grows with |v| in the negative tail, where the
+ *              value vanishes: about 10^-6 at v = -20)
  *   M, R       [n_tok][d_out] in y_dtype (device, 16-byte aligned) or NULL: a
  *              factor (the other branch of a gated MLP) and a residual; either
  *              may be Y itself
