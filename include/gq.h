@@ -442,7 +442,7 @@ gq_status gq_rmsnorm_quantize_int8(const void *X, const void *R, gq_dtype x_dtyp
  *   act        GQ_ACT_NONE, GQ_ACT_RELU, GQ_ACT_GELU (tanh form) or
  *              GQ_ACT_SILU (v / (1 + e^-v)); NaN stays NaN.  GELU and SiLU
  *              use the hardware's approximate exponential and reciprocal, for
- *              fp32 Y too: within 2^-21 of the value or 2^-20 absolutely (the
+ *              fp32 Y too: within 2^-21 of the value and another 2^-20 (the
  *              relative error grows with |v| in the negative tail, where the
  *              value vanishes: about 10^-6 at v = -20)
  *   M, R       [n_tok][d_out] in y_dtype (device, 16-byte aligned) or NULL: a
