@@ -385,6 +385,8 @@ gq_status gq_qlinear_bf16(const uint32_t *qpacked, const uint16_t *scales,
  *   scales     [n_tok] fp32 (device, out)
  *   sums       [n_tok] int32 (device, out) or NULL: sum_k c_k, which the
  *              product with affine weights needs
+ * Outputs that overlap an input or one another are refused (GQ_ERR_ARG), here
+ * and in the product below, but for the places named.
  *
  * gq_quantize_tokens_int8: g = X, or X * col_mul in fp32.
  *   col_mul    [d_in] fp32 factor per input column (device, 16-byte aligned)

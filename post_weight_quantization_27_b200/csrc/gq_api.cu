@@ -2,6 +2,7 @@
 // sizing, and dispatch to the kernels.  See include/gq.h for the contract.
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "gq_device.cuh"
@@ -452,6 +453,34 @@ bool partly_overlap(const void *a, const void *b, uint64_t bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a && b && x != y && (x < y ? y - x : x - y) < bytes;
 }
+// A range of device memory, `rows` times `bytes`, `pitch` bytes apart.
+struct Range {
+  const void *p;
+  uint64_t bytes, rows = 1, pitch = 0;
+};
+// Whether the dense range `out` shares a byte with `in`.
+bool overlap(const Range &out, const Range &in) {
+  if (!out.p || !in.p || !out.bytes || !in.bytes || !in.rows) return false;
+  const uintptr_t o = reinterpret_cast<uintptr_t>(out.p), i = reinterpret_cast<uintptr_t>(in.p);
+  if (o + out.bytes <= i) return false;
+  // the first row of `in` that ends behind out's start
+  uint64_t row = 0;
+  if (o >= i + in.bytes) {
+    if (in.rows == 1) return false;
+    row = (o - i - in.bytes) / in.pitch + 1;
+  }
+  return row < in.rows && i + row * in.pitch < o + out.bytes;
+}
+// GQ_OK when no output overlaps an input or another output.
+gq_status check_apart(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+  for (const Range *o = outs.begin(); o != outs.end(); ++o) {
+    for (const Range &i : ins)
+      if (overlap(*o, i)) return fail(GQ_ERR_ARG, "an output overlaps an input");
+    for (const Range *q = outs.begin(); q != o; ++q)
+      if (overlap(*o, *q)) return fail(GQ_ERR_ARG, "two outputs overlap");
+  }
+  return GQ_OK;
+}
 }  // namespace
 
 gq_status gq_quantize_tokens_int8(const void *X, gq_dtype x_dtype, int64_t n_tok, int64_t d_in,
@@ -465,6 +494,9 @@ gq_status gq_quantize_tokens_int8(const void *X, gq_dtype x_dtype, int64_t n_tok
     return fail(GQ_ERR_SHAPE, "ldx must be at least d_in, with rows a multiple of 16 bytes long");
   if (!aligned(X, 16) || !aligned(col_mul, 16) || !aligned(codes, 16))
     return fail(GQ_ERR_ARG, "X, col_mul and codes must be 16-byte aligned");
+  const uint64_t n = n_tok, e = dtype_size(x_dtype);
+  GQ_TRY(check_apart({{codes, n * d_in}, {scales, 4 * n}, {sums, 4 * n}},
+                     {{X, d_in * e, n, ldx * e}, {col_mul, 4 * static_cast<uint64_t>(d_in)}}));
   return launch_quant_int8(X, nullptr, x_dtype, n_tok, d_in, ldx, col_mul, GQ_F32, 0, 0.0f,
                            nullptr, codes, scales, sums, static_cast<cudaStream_t>(stream));
 }
@@ -488,6 +520,10 @@ gq_status gq_rmsnorm_quantize_int8(const void *X, const void *R, gq_dtype x_dtyp
   const uint64_t bytes = static_cast<uint64_t>(n_tok) * d_in * dtype_size(x_dtype);
   if (partly_overlap(H_out, X, bytes) || partly_overlap(H_out, R, bytes))
     return fail(GQ_ERR_ARG, "H_out must be X, R or a range of its own");
+  const uint64_t n = n_tok, wb = d_in * dtype_size(w_dtype);
+  GQ_TRY(check_apart({{codes, n * d_in}, {scales, 4 * n}, {sums, 4 * n}},
+                     {{X, bytes}, {R, bytes}, {H_out, bytes}, {weight, wb}}));
+  GQ_TRY(check_apart({{H_out, bytes}}, {{weight, wb}}));
   return launch_quant_int8(X, R, x_dtype, n_tok, d_in, d_in, weight, w_dtype, 1, eps, H_out, codes,
                            scales, sums, static_cast<cudaStream_t>(stream));
 }
@@ -508,6 +544,11 @@ gq_status gq_unpack_int8(const uint32_t *qpacked, const uint16_t *zeros, int64_t
   const uint64_t qn = static_cast<uint64_t>(d_out) * d_in * bits / 8, cn = static_cast<uint64_t>(d_out) * d_in;
   if (q0 < c0 + cn && c0 < q0 + qn && !(bits == 8 && q0 == c0))
     return fail(GQ_ERR_ARG, "w_codes must not overlap qpacked (at 8 bits it may be qpacked itself)");
+  if (sym == 0) {
+    const uint64_t m = d_out;
+    GQ_TRY(check_apart({{w_codes, cn}, {w_zpoint, 4 * m}}, {{zeros, 2 * m}}));
+    GQ_TRY(check_apart({{w_zpoint, 4 * m}}, {{qpacked, qn}}));
+  }
   return launch_unpack_int8(qpacked, zeros, d_out, d_in, bits, w_codes, sym ? nullptr : w_zpoint,
                             static_cast<cudaStream_t>(stream));
 }
@@ -540,6 +581,10 @@ gq_status gq_w8a8_matmul(const int8_t *w_codes, const uint16_t *w_scales, const 
   if (partly_overlap(Y, M, bytes) || partly_overlap(Y, R, bytes))
     return fail(GQ_ERR_ARG, "Y must be M, R or a range of its own");
   GQ_TRY(check_ws(ws, ws_bytes, kWsHeader));
+  const uint64_t n = n_tok, m = d_out, k = d_in;
+  GQ_TRY(check_apart({{Y, bytes}},
+                     {{w_codes, m * k}, {w_scales, 2 * m}, {w_zpoint, 4 * m}, {x_codes, n * k},
+                      {x_scales, 4 * n}, {w_zpoint ? x_sums : nullptr, 4 * n}, {bias, 4 * m}}));
   return launch_w8a8(w_codes, w_scales, w_zpoint, d_out, d_in, x_codes, x_scales, x_sums, n_tok,
                      bias, act, M, R, Y, y_dtype, static_cast<int *>(ws),
                      static_cast<cudaStream_t>(stream));

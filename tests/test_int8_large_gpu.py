@@ -98,6 +98,17 @@ def test_quantize_rows_of_wider_ones_and_nothing_outside(n, d):
         assert bool((t[:2] == v).all()) and bool((t[n + 2:] == v).all())
 
 
+def test_codes_between_the_rows_of_wider_ones():
+    """Codes, scales and sums in the part of X's rows that the call does not read."""
+    big = _big(3, 1024, "bf16", 4, special=False)
+    X, raw = big[:, :64], big.view(torch.int8)
+    out = dict(codes=raw[0, 128:320].view(3, 64), scales=raw[1, 128:140].view(torch.float32),
+               sums=raw[2, 2036:].view(torch.int32))
+    c, s, cs = _rows_int8(X.float())
+    gq.quantize_tokens_int8(X, out=out)
+    assert torch.equal(out["codes"], c) and torch.equal(out["scales"], s) and torch.equal(out["sums"], cs)
+
+
 def _check_norm(q, X, w, eps, R, sums):
     d = X.shape[1]
     h = X if R is None else (X.float() + R.float()).to(X.dtype)
