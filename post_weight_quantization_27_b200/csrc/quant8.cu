@@ -365,12 +365,12 @@ __device__ __forceinline__ int put(uint64_t (&g)[P], const RowGrid &gr, int8_t *
 // `team` threads take a row (or a slice of at most 8192 elements of one: the
 // CTAs of a cluster share a longer row), N elements each, all loads first.
 // N = 8 for a few tokens: the time is one load's latency, the reductions and
-// the launch (one token of 4096: 1.9 us in a graph, 2.6 with residual and
+// the launch (one token of 4096: 1.7 us in a graph, 2.4 with residual and
 // norm).  N = 32 while the rows fit the SMs at once, and for rows that the
 // persistent kernel cannot hold (16 elements per thread were 4 to 13% faster
 // around 4M elements and slower on both sides of that: not kept).  Measured
-// (bf16, graph replays): 150 x 768, N = 8, plain 1.5 us, norm 2.0; N = 32: 512
-// x 4096 plain 3.3 us, norm 5.3, 100 x 28672 norm with residual 8.2 us.
+// (bf16, graph replays): 150 x 768, N = 8, plain 1.6 us, norm 2.0; N = 32: 512
+// x 4096 plain 3.3 us, norm 5.1, 100 x 28672 norm with residual 8.4 us.
 constexpr int kSlice = 8192;
 
 template <typename T, typename WT, Mode MODE, int N>
@@ -459,11 +459,11 @@ __global__ void __launch_bounds__(N == 8 ? 1024 : 256, N == 8 ? 1 : 3) quant_blo
 // registers, and spill: 54% of the copy bandwidth instead of 77% when it was
 // tried).  One barrier per row: the codes' sums of a row are added up behind
 // the next row's.  x (and r) are read, codes (and h) written: plain rows and
-// fp32 rows are bound by HBM (16384 x 28672 bf16 204 us = 105% of the copy
+// fp32 rows are bound by HBM (16384 x 28672 bf16 205 us = 105% of the copy
 // bandwidth, 16384 x 8192 fp32 with factors 104 us = 99%), 16-bit rows with
 // factors also by the instructions issued, 14 an element with column factors,
 // 21 with the norm and 27 with its residual against 12 plain (16384 x 28672
-// 263 us = 82%, 32768 x 8192 norm with residual 306 us = 94%, without 216 us
+// 264 us = 82%, 32768 x 8192 norm with residual 312 us = 92%, without 216 us
 // = 57%).
 constexpr int kRegThreads = 640;
 constexpr size_t kRingMost = 225 * 1024;
@@ -483,7 +483,7 @@ __device__ __forceinline__ void sts16(uint32_t p, const uint4 &v) {
 
 // FULL: every thread has all its units (d_in = 32 team), so that no unit is a
 // branch of its own.  For 16-bit rows with column factors, which are bound by
-// the instructions issued: 16384 x 28672 278 -> 263 us (plain rows, bound by
+// the instructions issued: 16384 x 28672 278 -> 264 us (plain rows, bound by
 // HBM, 220 -> 250: not there).
 template <typename T, typename WT, Mode MODE, int AHEAD, bool WREG, bool FULL>
 __global__ void __launch_bounds__(WREG ? kRegThreads : 1024, 1) quant_rows_kernel(const QuantArgs a) {
@@ -693,9 +693,12 @@ gq_status launch_rows(QuantArgs a, cudaStream_t st) {
   cudaError_t e;
   // Measured (graph replays, inputs from HBM): 8 elements per thread while a
   // row has an SM of its own or all rows together take few of its threads
-  // (600 x 768 fp32 2.7 us, 32 per thread 3.4); 32 per thread in one wave
-  // of blocks (512 x 4096 bf16 3.7 us, 8 per thread 4.7, persistent 4.1);
-  // persistent beyond (4000 x 2048 fp32 10.2 us, a block per row 12.5).
+  // (600 x 768 fp32 2.3 us, 32 per thread 3.0); 32 per thread in one wave
+  // of blocks (512 x 4096 bf16 3.3 us, 8 per thread 4.3, persistent 3.6);
+  // persistent beyond (4000 x 2048 fp32 9.7 us, a block per row 11.8).
+  // Between 4M and 12M elements the persistent blocks make one round, so that
+  // they copy their factors once for a row or two: norm of 2047 x 2048 fp16
+  // 7.9 us, by a block per row 8.2 (N = 8) and 9.0 (32).
   const int64_t elems = a.n_tok * a.d_in, sms = num_sms();
   if (a.n_tok * a.split <= sms || elems <= sms * 512 * 8)
     e = launch_block<T, WT, MODE, 8>(a, st);
