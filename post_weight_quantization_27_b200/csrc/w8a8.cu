@@ -685,9 +685,13 @@ __global__ void __launch_bounds__(PairShape<PJ, TMA>::kThreads, 1)
 // additions does not matter, no workspace and no second launch.
 // A lane owns an output, so a warp's accesses to Y, M and R are contiguous
 // whatever d_out is.  Bound by the weights' way from HBM and by what comes
-// before and after it (set-up, the first bytes, the sums' exchange, Y: about
-// 7 us): 33 x 8192 x 8192 18.6 us (10.4 at the copy rate; 16384 inputs take
-// 11.2 us more, 6.0 TB/s), 16 x 4096 x 11008 12.5 us.
+// before and after it: 33 x 8192 x 8192 affine with residual 19.5 us (10.5 at
+// the copy rate; 16384 inputs take 11.6 us more, 5.8 TB/s), 16 x 4096 x 11008
+// 12.2, 33 x 4096 x 4096 9.2 (2.6 at the copy rate).  So about 7 us are this
+// kernel's own (the dp4a kernel pays 2 around the same weights): TMEM, barriers
+// and the first round of the ring, then the sums' exchange, which few_us puts
+// at 1.5 us and 0.06 a token of the tile: each CTA reads them by 4-byte loads
+// from the others between two cluster barriers.
 constexpr int F_J = 128, F_T = 128, F_MAX_STAGES = 12, F_THREADS = 128;
 
 struct FewPlan {
@@ -914,7 +918,7 @@ __global__ void __launch_bounds__(F_THREADS)
 // with NT tokens by dp4a; `ks` warps of a block share a row group along K and
 // add up through shared memory.  No barriers, no TMEM and no tensor maps to set up: the
 // weights' bytes and one memory round trip are all there is.  HBM-bound: one
-// token 4096 -> 11008 9.5 us of 6.9 at the copy rate, 8192 -> 28672 36.2 of
+// token 4096 -> 11008 9.5 us of 6.9 at the copy rate, 8192 -> 28672 36.5 of
 // 35.9, 768 -> 2304 2.1 us.  The
 // first steps' weights start towards L2 before the stream's earlier work is
 // done (whose results they may be: nothing is read yet): behind a token's norm
