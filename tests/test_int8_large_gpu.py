@@ -2,6 +2,11 @@
 persistent kernels over several rounds of rows and tiles, a block per row of 32 elements per thread,
 and GPTQ's layers.  The reference is the definition in elementary torch operations on the GPU (codes
 in IEEE fp32, which defines them, the rest in 64 bits), the oracle on some of the rows."""
+import os
+import subprocess
+import sys
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 import torch
@@ -221,6 +226,56 @@ def test_product_of_prompts(n, d, m, dt):
     _product(n, d, m, dt)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n,m", [(1, 40), (5, 333), (37, 333), (130, 640), (1300, 4000), (1300, 4001)])
+def test_product_that_is_its_own_factor_and_residual(n, m, dt):
+    g = torch.Generator().manual_seed(n + m)
+    (wc, ws, _), (xc, xs, _) = _layer(m, 272, False, g), _tokens(n, 272, g)
+    w, x = dict(codes=wc.cuda(), scales=ws.cuda()), dict(codes=xc.cuda(), scales=xs.cuda())
+    M = torch.randn(n, m, generator=g).to(DT[dt]).cuda()
+    want = gq.w8a8_matmul(w, x, act="relu", mul=M.clone(), R=M.clone(), dtype=DT[dt])
+    Y = M.clone()
+    assert gq.w8a8_matmul(w, x, act="relu", mul=Y, R=Y, Y=Y) is Y and torch.equal(Y, want)
+
+
+# ------------------------------------------------------------------ offsets beyond 32 bits
+
+def test_tokens_beyond_2_31_elements():
+    n, d = 75011, 28672
+    X = torch.zeros(n, d, dtype=torch.bfloat16, device="cuda")
+    rows = [0, 1, 37449, 37450, 74897, 74898, 74899, n - 2, n - 1]
+    X[rows] = _big(len(rows), d, "bf16", 6, special=False)
+    w = torch.linspace(0.5, 1.5, d, device="cuda")
+    Xr = X[rows]
+    for col in (None, w):
+        q = gq.quantize_tokens_int8(X, col)
+        c, s, cs = _rows_int8(Xr.float() if col is None else Xr.float() * col)
+        assert torch.equal(q["codes"][rows], c) and torch.equal(q["scales"][rows], s)
+        assert torch.equal(q["sums"][rows], cs) and int((q["sums"] != 0).sum()) <= len(rows)
+        del q
+    for R in (None, X):
+        q = gq.rmsnorm_quantize_int8(X, w, R=R)
+        assert int((q["sums"] != 0).sum()) <= len(rows)
+        # (the scales by their bound: another kernel takes the rows alone, and adds in another order)
+        _check_norm({k: v[rows] for k, v in q.items()}, Xr, w, 1e-5, None if R is None else Xr, True)
+        del q
+
+
+@pytest.mark.parametrize("m", [32768, 32777])
+def test_products_beyond_2_31_outputs(m):
+    n, d = 65577, 48
+    g = torch.Generator().manual_seed(m)
+    (wc, ws, _), (xc, xs, _) = _layer(m, d, False, g), _tokens(n, d, g)
+    w, x = dict(codes=wc.cuda(), scales=ws.cuda()), dict(codes=xc.cuda(), scales=xs.cuda())
+    R = torch.zeros(n, m, dtype=torch.bfloat16, device="cuda")
+    R[-9:] = 1.5
+    Y = gq.w8a8_matmul(w, x, act="silu", R=R)
+    for at in (0, 32768, 65400, n - 300):
+        part = {k: v[at:at + 300].clone() for k, v in x.items()}
+        assert torch.equal(Y[at:at + 300], gq.w8a8_matmul(w, part, act="silu",
+                                                          R=R[at:at + 300].clone()))
+
+
 # ------------------------------------------------------------------ used together
 
 def test_calls_behind_one_another_see_each_others_results():
@@ -263,6 +318,53 @@ def test_calls_behind_one_another_see_each_others_results():
         torch.cuda.synchronize()
         assert torch.equal(x, ref[0]) and torch.equal(h, ref[1])
     del graph
+
+
+_FIRST = """
+import torch
+from post_weight_quantization_27_b200 import gq
+w = dict(codes=torch.ones(4096, 256, dtype=torch.int8, device="cuda"),
+         scales=torch.ones(4096, 1, dtype=torch.float16, device="cuda"))
+nw = torch.ones(256, device="cuda")
+out = []
+g = torch.cuda.CUDAGraph()
+xs = [torch.ones(n, 256, device="cuda") for n in (1, 40, 1300)]
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    for x in xs:
+        q = gq.rmsnorm_quantize_int8(x, nw, R=x)
+        out.append(gq.w8a8_matmul(w, gq.quantize_tokens_int8(q["h"]), dtype=torch.float32))
+g.replay()
+torch.cuda.synchronize()
+assert all(bool((y - 512.0).abs().max() < 1e-3) for y in out)
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    r = subprocess.run([sys.executable, "-c", _FIRST], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_threads_call_at_once():
+    """Two host threads, each with a stream and tensors of its own."""
+    d = 512
+    w, _, _ = _mlp_layers(d, d)
+    nw = torch.ones(d, device="cuda")
+    X = [_big(n, d, "bf16", n, special=False) for n in (7, 1100)]
+
+    def chain(x, s):
+        with torch.cuda.stream(s):
+            for _ in range(30):
+                q = gq.rmsnorm_quantize_int8(x, nw)
+                x = gq.w8a8_matmul(w, q, R=x)
+        s.synchronize()
+        return x
+    want = [chain(x, torch.cuda.current_stream()) for x in X]
+    with ThreadPoolExecutor(2) as pool:
+        for _ in range(5):
+            got = list(pool.map(chain, X, [torch.cuda.Stream(), torch.cuda.Stream()]))
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 # ------------------------------------------------------------------ layers of GPTQ
